@@ -122,8 +122,10 @@ enum {
   DS_ERR_CAPTURE = -8, /* reserved: no call returns it (a ragged weight call
                           on a capturing stream splits its launches instead;
                           see ds_weight_rownorm_gain) */
-  DS_ERR_SCRATCH = -9  /* an allocation-free call needs more of the library's
+  DS_ERR_SCRATCH = -9, /* an allocation-free call needs more of the library's
                           fixed scratch than DS_SCRATCH_FLOATS */
+  DS_ERR_WORKSPACE = -10 /* the caller's workspace is smaller than the call's
+                          _workspace function says (ds_token_rows.h) */
 };
 
 /*

@@ -1,4 +1,5 @@
-"""ctypes binding of libdsrows.so (include/ds_rows.h): argument marshalling only.
+"""ctypes binding of libdsrows.so (include/ds_rows.h, include/ds_token_rows.h):
+argument marshalling only.
 
 Every computation runs in the library's HIP kernels.  The functions take
 torch tensors on a HIP device, check dtype/shape/contiguity/device, pass raw
@@ -14,13 +15,14 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import List, Optional, Sequence, Tuple
+from typing import List, NamedTuple, Optional, Sequence, Tuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 # DS_ROWS_LIB may name another build of the same library (the tests'
 # AddressSanitizer build of the host code); there is no fallback either way
 LIB_PATH = os.environ.get("DS_ROWS_LIB") or os.path.join(PKG, "_lib", "libdsrows.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "ds_rows.h")
+TOKEN_HEADER = os.path.join(os.path.dirname(PKG), "include", "ds_token_rows.h")
 
 DS_OK = 0
 DS_ERR_NULL = -1
@@ -32,7 +34,10 @@ DS_ERR_LAUNCH = -6
 DS_ERR_DEVICE = -7
 DS_ERR_CAPTURE = -8
 DS_ERR_SCRATCH = -9
+DS_ERR_WORKSPACE = -10
 DS_SCRATCH_FLOATS = 1 << 20
+DS_MAX_TOP = 32
+DS_TYPE_BF16, DS_TYPE_F32 = 0, 1
 
 
 class RownormDesc(ctypes.Structure):
@@ -83,6 +88,7 @@ class RescaleDesc(ctypes.Structure):
 
 
 _lib = None
+_token = False
 
 
 def lib() -> ctypes.CDLL:
@@ -133,9 +139,46 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def header_functions() -> List[str]:
-    """Names of the functions include/ds_rows.h declares."""
-    text = open(HEADER).read()
+def _token_lib() -> ctypes.CDLL:
+    """The library with ds_token_rows.h's entry points declared; raises if the
+    loaded build does not hold them."""
+    global _token
+    L = lib()
+    if not _token:
+        vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+        sig = {
+            "ds_embed_rows": [vp, i32, i64, vp, i32, f32, vp, i64, i64, vp],
+            "ds_embed_rows_backward": [vp, vp, i32, f32, vp, i32, i32, i64, i64, i64, vp, i64, vp],
+            "ds_qk_rows_rms": [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i64, i32, i32,
+                               i32, f32, vp],
+            "ds_qk_rows_rms_backward": [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64,
+                                        vp, i64, vp, vp, i64, i32, i32, i32, f32, vp, i64, vp],
+            "ds_logprob_rows": [vp, i32, i64, vp, f32, vp, i32, vp, vp, vp, vp, vp, i32, i64, i64,
+                                vp, i64, vp],
+            "ds_logprob_rows_backward": [vp, i32, i64, vp, f32, vp, i32, vp, vp, vp, vp, vp, i64, vp,
+                                         i64, i64, vp, i64, vp],
+        }
+        sizes = {
+            "ds_embed_rows_backward_workspace": [i64, i64, i64],
+            "ds_qk_rows_rms_backward_workspace": [i64, i32, i32, i32],
+            "ds_logprob_rows_workspace": [i64, i64, i32],
+            "ds_logprob_rows_backward_workspace": [i64, i64],
+        }
+        for table, res in ((sig, ctypes.c_int), (sizes, i64)):
+            for name, args in table.items():
+                try:
+                    f = getattr(L, name)
+                except AttributeError:
+                    raise RuntimeError(f"{LIB_PATH} does not hold {name}: build the library again "
+                                       "with `python -m scale_invariant_row_amd.build`") from None
+                f.argtypes, f.restype = args, res
+        _token = True
+    return L
+
+
+def header_functions(header: str = HEADER) -> List[str]:
+    """Names of the functions a header (include/ds_rows.h) declares."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(ds_\w+)\s*\(", text, re.M)))
 
@@ -624,3 +667,349 @@ def ds_rescale_after_step(ws: Sequence, moms: Optional[Sequence] = None,
                           segs: Optional[Sequence] = None) -> None:
     """In place, per matrix: project the momentum (if given), then w <- radius w/||w||."""
     _rescale(ws, moms, radius, True, stream, segs)
+
+
+# ------------------------------------------------------------- token rows
+
+def _launch_on(t, stream):
+    """Contexts of a call on tensor t: its device, and the launch stream as
+    torch's current one, so what is allocated inside belongs to that stream."""
+    torch = _torch()
+    import contextlib
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(t.device))
+    if stream is not None:
+        ctx.enter_context(torch.cuda.stream(_torch_stream(t, stream)))
+    return ctx
+
+
+def _workspace(nbytes: int, what: str, device):
+    """Scratch memory of a call, on the launch stream: dropped after the call,
+    its block is handed only to work ordered after the call's kernels."""
+    if nbytes < 0:
+        _check(nbytes, what)
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if nbytes else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _value_type(t, name: str) -> int:
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return DS_TYPE_F32
+    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return DS_TYPE_BF16
+    raise TypeError(f"{name}: expected fp32 or bf16 data, got {t.dtype}")
+
+
+def _ids(t, name: str, rows: Optional[int] = None) -> int:
+    torch = _torch()
+    if t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 or not t.is_contiguous() \
+            or (rows is not None and t.shape[0] != rows):
+        want = "[rows]" if rows is None else f"[{rows}]"
+        raise ValueError(f"{name}: expected a contiguous int32 or int64 {want} tensor")
+    return 8 if t.dtype == torch.int64 else 4
+
+
+def _vec(t, name: str, n: int, dtype=None):
+    dtype = _torch().float32 if dtype is None else dtype
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {dtype} [{n}] tensor")
+
+
+def _on_device_of(first, name: str, others):
+    if first.device.type != "cuda":
+        raise ValueError(f"{name}: must be on a HIP device")
+    for t, n in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{n}: must be on the HIP device of {name}")
+
+
+def ds_embed_rows(table, ids, scale: float = 1.0, out=None, stream=None):
+    """out_i = bf16(scale * table[ids_i]) (bf16 [rows, cols]).
+
+    ``table``: fp32 or bf16 [vocab, cols]; ``ids``: int32 or int64 [rows].  An
+    id outside the table gives a row of zeros.
+    """
+    torch = _torch()
+    kind = _value_type(table, "table")
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table: expected a contiguous [vocab, cols] tensor")
+    id_bytes = _ids(ids, "ids")
+    rows, (vocab, cols) = ids.shape[0], table.shape
+    if out is not None:
+        _bf16_2d(out, "out", device=False)
+        if tuple(out.shape) != (rows, cols):
+            raise ValueError(f"out: expected [{rows}, {cols}]")
+    _on_device_of(table, "table", [(ids, "ids"), (out, "out")])
+    with _launch_on(table, stream):
+        if out is None:
+            out = torch.empty(rows, cols, dtype=torch.bfloat16, device=table.device)
+        st = _token_lib().ds_embed_rows(table.data_ptr(), kind, vocab, ids.data_ptr(), id_bytes,
+                                        float(scale), out.data_ptr(), rows, cols,
+                                        _stream_of(table, stream))
+    _check(st, "ds_embed_rows")
+    return out
+
+
+def ds_embed_rows_backward(dy, ids, vocab: int, scale: float = 1.0, dtable=None, dtype=None,
+                           accumulate: bool = False, stream=None):
+    """dtable[t] = scale * sum of dy_i over the rows with ids_i == t.
+
+    ``dtable`` ([vocab, cols], fp32 or bf16) is allocated as ``dtype`` (fp32
+    when not given) and written whole; with ``accumulate`` the sums are added
+    to a given ``dtable`` and the rows of absent tokens stay as they are.
+    Returns ``dtable``.
+    """
+    torch = _torch()
+    _bf16_2d(dy, "dy", device=False)
+    rows, cols = dy.shape
+    id_bytes = _ids(ids, "ids", rows)
+    vocab = int(vocab)
+    if vocab < 0:
+        raise ValueError("vocab: must not be negative")
+    if dtable is not None:
+        if dtype is not None and dtable.dtype != dtype:
+            raise ValueError("dtable: has another dtype than the one asked for")
+        if tuple(dtable.shape) != (vocab, cols) or not dtable.is_contiguous():
+            raise ValueError(f"dtable: expected a contiguous [{vocab}, {cols}] tensor")
+        _value_type(dtable, "dtable")
+    elif accumulate:
+        raise ValueError("dtable: accumulate needs one")
+    elif dtype not in (None, torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype: expected fp32 or bf16, got {dtype}")
+    _on_device_of(dy, "dy", [(ids, "ids"), (dtable, "dtable")])
+    L = _token_lib()
+    with _launch_on(dy, stream):
+        if dtable is None:
+            dtable = torch.empty(vocab, cols, dtype=dtype or torch.float32, device=dy.device)
+        nbytes = L.ds_embed_rows_backward_workspace(vocab, rows, cols)
+        ws = _workspace(nbytes, "ds_embed_rows_backward", dy.device)
+        st = L.ds_embed_rows_backward(dy.data_ptr(), ids.data_ptr(), id_bytes, float(scale),
+                                      dtable.data_ptr(), _value_type(dtable, "dtable"),
+                                      int(bool(accumulate)), vocab, rows, cols, _ptr(ws), nbytes,
+                                      _stream_of(dy, stream))
+    _check(st, "ds_embed_rows_backward")
+    return dtable
+
+
+def _heads(t, name: str, head_dim: int, rows: Optional[int] = None) -> int:
+    """Number of heads of a bf16 [rows, heads * head_dim] view (rows may be strided)."""
+    torch = _torch()
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or t.dim() != 2 \
+            or (t.numel() > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a bf16 [rows, cols] tensor with unit column stride")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{name}: expected {rows} rows like q, got {t.shape[0]}")
+    if t.shape[1] % head_dim:
+        raise ValueError(f"{name}: its width must be a whole number of heads")
+    return t.shape[1] // head_dim
+
+
+def _row_stride(t) -> int:
+    """A view's row stride; a lone row's may be anything, and is not read."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _qk_rms_checks(q, k, positions, inv_freq, q_weight, k_weight, head_dim):
+    torch = _torch()
+    if head_dim <= 0:
+        raise ValueError("head_dim: must be positive")
+    nq = _heads(q, "q", head_dim)
+    nk = _heads(k, "k", head_dim, q.shape[0]) if k is not None else 0
+    _vec(positions, "positions", q.shape[0], torch.int32)
+    _vec(inv_freq, "inv_freq", head_dim // 2)
+    _vec(q_weight, "q_weight", head_dim)
+    _vec(k_weight, "k_weight", head_dim)
+    return nq, nk
+
+
+def _like_heads(t, like, name: str, head_dim: int, rows: int, heads: int):
+    """A given output or gradient must hold exactly the heads of ``like``."""
+    if t is None:
+        return
+    if like is None:
+        raise ValueError(f"{name}: given without k")
+    if _heads(t, name, head_dim, rows) != heads:
+        raise ValueError(f"{name}: expected [{rows}, {heads * head_dim}]")
+
+
+def ds_qk_rows_rms(q, k, positions, inv_freq, q_weight, k_weight, head_dim: int,
+                   eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Each head's RMS norm times a learned weight, then rotate-half RoPE, on
+    q [rows, nq * head_dim] and k [rows, nk * head_dim] (k may be None).
+
+    ``q``/``k`` may be strided row views (a fused projection's slices);
+    ``positions``: int32 [rows]; ``inv_freq``: fp32 [head_dim / 2]; weights:
+    fp32 [head_dim] or None (1).  Returns (q_out, k_out); the outputs may be
+    the inputs themselves.
+    """
+    torch = _torch()
+    head_dim = int(head_dim)
+    nq, nk = _qk_rms_checks(q, k, positions, inv_freq, q_weight, k_weight, head_dim)
+    rows = q.shape[0]
+    _like_heads(q_out, q, "q_out", head_dim, rows, nq)
+    _like_heads(k_out, k, "k_out", head_dim, rows, nk)
+    _on_device_of(q, "q", [(k, "k"), (positions, "positions"), (inv_freq, "inv_freq"),
+                           (q_weight, "q_weight"), (k_weight, "k_weight"), (q_out, "q_out"),
+                           (k_out, "k_out")])
+    with _launch_on(q, stream):
+        if q_out is None:
+            q_out = torch.empty(rows, nq * head_dim, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(rows, nk * head_dim, dtype=k.dtype, device=k.device)
+        ld = lambda t: 0 if t is None else _row_stride(t)  # noqa: E731
+        st = _token_lib().ds_qk_rows_rms(
+            q.data_ptr(), ld(q), _ptr(k), ld(k), positions.data_ptr(), inv_freq.data_ptr(),
+            _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(), ld(q_out), _ptr(k_out), ld(k_out),
+            rows, nq, nk, head_dim, float(eps), _stream_of(q, stream))
+    _check(st, "ds_qk_rows_rms")
+    return q_out, k_out
+
+
+def ds_qk_rows_rms_backward(q, k, positions, inv_freq, q_weight, k_weight, dq_out, dk_out,
+                            head_dim: int, eps: float = 1e-6, dq=None, dk=None,
+                            want_dweights: bool = True, stream=None):
+    """The gradient of ds_qk_rows_rms(q, k, ...) from the gradients reaching
+    its outputs.  Returns (dq, dk, dq_weight, dk_weight): bf16 like q and k
+    (``dq`` may be ``dq_out`` or ``q``, ``dk`` likewise), the weights' fp32
+    [head_dim], or None without ``want_dweights`` (and for k without k).
+    """
+    torch = _torch()
+    head_dim = int(head_dim)
+    nq, nk = _qk_rms_checks(q, k, positions, inv_freq, q_weight, k_weight, head_dim)
+    rows = q.shape[0]
+    _like_heads(dq_out, q, "dq_out", head_dim, rows, nq)
+    if k is not None and dk_out is None:
+        raise ValueError("dk_out: missing")
+    _like_heads(dk_out, k, "dk_out", head_dim, rows, nk)
+    _like_heads(dq, q, "dq", head_dim, rows, nq)
+    _like_heads(dk, k, "dk", head_dim, rows, nk)
+    _on_device_of(q, "q", [(k, "k"), (positions, "positions"), (inv_freq, "inv_freq"),
+                           (q_weight, "q_weight"), (k_weight, "k_weight"), (dq_out, "dq_out"),
+                           (dk_out, "dk_out"), (dq, "dq"), (dk, "dk")])
+    L = _token_lib()
+    with _launch_on(q, stream):
+        if dq is None:
+            dq = torch.empty(rows, nq * head_dim, dtype=q.dtype, device=q.device)
+        if k is not None and dk is None:
+            dk = torch.empty(rows, nk * head_dim, dtype=k.dtype, device=k.device)
+        dqw = dkw = ws = None
+        nbytes = 0
+        if want_dweights:
+            dqw = torch.empty(head_dim, dtype=torch.float32, device=q.device)
+            dkw = torch.empty_like(dqw) if k is not None else None
+            nbytes = L.ds_qk_rows_rms_backward_workspace(rows, nq, nk, head_dim)
+            ws = _workspace(nbytes, "ds_qk_rows_rms_backward", q.device)
+        ld = lambda t: 0 if t is None else _row_stride(t)  # noqa: E731
+        st = L.ds_qk_rows_rms_backward(
+            q.data_ptr(), ld(q), _ptr(k), ld(k), positions.data_ptr(), inv_freq.data_ptr(),
+            _ptr(q_weight), _ptr(k_weight), dq_out.data_ptr(), ld(dq_out), _ptr(dk_out), ld(dk_out),
+            dq.data_ptr(), ld(dq), _ptr(dk), ld(dk), _ptr(dqw), _ptr(dkw), rows, nq, nk, head_dim,
+            float(eps), _ptr(ws), nbytes, _stream_of(q, stream))
+    _check(st, "ds_qk_rows_rms_backward")
+    return dq, dk, dqw, dkw
+
+
+class LogprobRows(NamedTuple):
+    """What ds_logprob_rows returns: fp32 [rows] each; the top alternatives'
+    int32 ids and fp32 log probabilities, [rows, top_k]."""
+    logp: object
+    entropy: object
+    lse: object
+    top_ids: object
+    top_logp: object
+
+
+def _logits(t, name: str):
+    kind = _value_type(t, name)
+    if t.dim() != 2 or (t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a [rows, vocab] tensor with unit column stride")
+    rows, vocab = t.shape
+    return kind, rows, vocab, (t.stride(0) if rows > 1 else vocab)
+
+
+def ds_logprob_rows(logits, labels=None, scale=None, inv_temp: float = 1.0, top_k: int = 0,
+                    stream=None) -> LogprobRows:
+    """Per row of logits [rows, vocab] (fp32 or bf16; rows may be strided): the
+    log probability of its label, the entropy, log sum exp, and the ``top_k``
+    largest tokens, of z = logits * scale * inv_temp.
+
+    ``labels``: int32 or int64 [rows], one outside the vocabulary marks a row
+    to ignore (logp 0); without labels logp is None.  ``scale``: fp32 [vocab]
+    or None.  top_ids and top_logp are None for top_k 0.
+    """
+    torch = _torch()
+    kind, rows, vocab, ld = _logits(logits, "logits")
+    label_bytes = 8 if labels is None else _ids(labels, "labels", rows)
+    _vec(scale, "scale", vocab)
+    top_k = int(top_k)
+    if not 0 <= top_k <= min(DS_MAX_TOP, vocab):
+        raise ValueError(f"top_k: expected 0 to {min(DS_MAX_TOP, vocab)}")
+    _on_device_of(logits, "logits", [(labels, "labels"), (scale, "scale")])
+    L = _token_lib()
+    with _launch_on(logits, stream):
+        new = lambda *shape, dtype=torch.float32: torch.empty(  # noqa: E731
+            *shape, dtype=dtype, device=logits.device)
+        logp = new(rows) if labels is not None else None
+        entropy, lse = new(rows), new(rows)
+        ids = new(rows, top_k, dtype=torch.int32) if top_k else None
+        top = new(rows, top_k) if top_k else None
+        nbytes = L.ds_logprob_rows_workspace(rows, vocab, top_k)
+        ws = _workspace(nbytes, "ds_logprob_rows", logits.device)
+        st = L.ds_logprob_rows(logits.data_ptr(), kind, ld, _ptr(scale), float(inv_temp),
+                               _ptr(labels), label_bytes, _ptr(logp), entropy.data_ptr(),
+                               lse.data_ptr(), _ptr(ids), _ptr(top), top_k, rows, vocab, _ptr(ws),
+                               nbytes, _stream_of(logits, stream))
+    _check(st, "ds_logprob_rows")
+    return LogprobRows(logp, entropy, lse, ids, top)
+
+
+def ds_logprob_rows_backward(logits, labels, lse, entropy, dlogp, dentropy=None, scale=None,
+                             inv_temp: float = 1.0, dlogits=None, want_dscale: bool = True,
+                             stream=None):
+    """The gradient of ds_logprob_rows' logp and entropy: (dlogits, dscale).
+
+    ``lse`` and ``entropy`` are the forward call's (entropy may be None
+    without ``dentropy``); ``dlogp``/``dentropy``: fp32 [rows] or None.
+    ``dlogits`` (like logits; may be logits itself) is allocated contiguous
+    when not given; dscale is None without ``scale`` or ``want_dscale``.
+    """
+    torch = _torch()
+    kind, rows, vocab, ld = _logits(logits, "logits")
+    label_bytes = 8 if labels is None else _ids(labels, "labels", rows)
+    if dlogp is not None and labels is None:
+        raise ValueError("labels: dlogp needs them")
+    if dentropy is not None and entropy is None:
+        raise ValueError("entropy: dentropy needs the forward call's")
+    if lse is None:
+        raise ValueError("lse: the forward call's is needed")
+    for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
+        _vec(t, n, rows)
+    _vec(scale, "scale", vocab)
+    ldo = vocab
+    if dlogits is not None:
+        if dlogits.dtype != logits.dtype or tuple(dlogits.shape) != (rows, vocab):
+            raise ValueError(f"dlogits: expected a [{rows}, {vocab}] tensor like logits")
+        ldo = _logits(dlogits, "dlogits")[3]
+    _on_device_of(logits, "logits", [(labels, "labels"), (lse, "lse"), (entropy, "entropy"),
+                                     (dlogp, "dlogp"), (dentropy, "dentropy"), (scale, "scale"),
+                                     (dlogits, "dlogits")])
+    L = _token_lib()
+    with _launch_on(logits, stream):
+        if dlogits is None:
+            dlogits = torch.empty(rows, vocab, dtype=logits.dtype, device=logits.device)
+        dscale = ws = None
+        nbytes = 0
+        if scale is not None and want_dscale:
+            dscale = torch.empty(vocab, dtype=torch.float32, device=logits.device)
+            nbytes = L.ds_logprob_rows_backward_workspace(rows, vocab)
+            ws = _workspace(nbytes, "ds_logprob_rows_backward", logits.device)
+        st = L.ds_logprob_rows_backward(
+            logits.data_ptr(), kind, ld, _ptr(scale), float(inv_temp), _ptr(labels), label_bytes,
+            lse.data_ptr(), _ptr(entropy), _ptr(dlogp), _ptr(dentropy), dlogits.data_ptr(), ldo,
+            _ptr(dscale), rows, vocab, _ptr(ws), nbytes, _stream_of(logits, stream))
+    _check(st, "ds_logprob_rows_backward")
+    return dlogits, dscale

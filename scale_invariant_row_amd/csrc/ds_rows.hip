@@ -489,6 +489,7 @@ const char* ds_status_string(int status) {
     case DS_ERR_DEVICE: return "DS_ERR_DEVICE: no usable HIP device";
     case DS_ERR_CAPTURE: return "DS_ERR_CAPTURE: reserved (a ragged call on a capturing stream now splits its launches instead)";
     case DS_ERR_SCRATCH: return "DS_ERR_SCRATCH: the call needs more library scratch than DS_SCRATCH_FLOATS (1,048,576 scalar-gain rows)";
+    case DS_ERR_WORKSPACE: return "DS_ERR_WORKSPACE: the workspace is smaller than the call needs";
     default: return "unknown ds_rows status";
   }
 }

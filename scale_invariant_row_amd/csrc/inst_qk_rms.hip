@@ -1,0 +1,306 @@
+// q/k heads: RMS norm with a learned weight, then rotate-half RoPE, and the
+// gradient.
+//
+//   u = x / D, D = sqrt(sum x^2 / HD + eps);  n = u w
+//   y = [n1 cos t - n2 sin t, n2 cos t + n1 sin t],  t_i = p inv_freq_i
+// and, with d = [dy1 cos t + dy2 sin t, dy2 cos t - dy1 sin t] (dy turned back):
+//   dw += d u,   dx = (w d - u <w d, u> / HD) / D
+//
+// A head spreads over LPH lanes (the power of two at or above HD / 16).  A
+// lane holds 8 values of the head's first half and the 8 they rotate with, so
+// the rotation needs no exchange between lanes and both loads are 16 bytes;
+// 64 / LPH heads go through the wave at a time.  Lanes past the head (a
+// head_dim that is no power of two) have their offsets out of the buffer's
+// range: loads return 0 and stores are dropped.
+//
+// Angles: the wave evaluates each of its row's HD/2 angles once and shares
+// them through LDS.  The turn p inv_freq / 2 pi is formed and reduced to
+// [-1/2, 1/2] in fp64 (exact to 1e-7 turns for any int32 position), its sine
+// and cosine in fp32.
+#include "row_kernels.hpp"
+#include "token_launch.hpp"
+
+namespace dsr {
+
+constexpr int kQkRmsOut = 0x7ffffff0;      // an offset past every buffer
+
+// Sum and maximum over the LPH lanes of a head.
+template <int LPH>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (LPH >= 2) v = v + dpp_f<0xB1>(v);
+  if constexpr (LPH >= 4) v = v + dpp_f<0x4E>(v);
+  if constexpr (LPH >= 8) v = v + dpp_f<0x141>(v);
+  if constexpr (LPH >= 16) v = v + dpp_f<0x140>(v);
+  return v;
+}
+
+template <int LPH>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (LPH >= 2) v = fmaxf(v, dpp_f<0xB1>(v));
+  if constexpr (LPH >= 4) v = fmaxf(v, dpp_f<0x4E>(v));
+  if constexpr (LPH >= 8) v = fmaxf(v, dpp_f<0x141>(v));
+  if constexpr (LPH >= 16) v = fmaxf(v, dpp_f<0x140>(v));
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(u32x4_t t, float* v) {
+  v[0] = bf_lo(t.x); v[1] = bf_hi(t.x); v[2] = bf_lo(t.y); v[3] = bf_hi(t.y);
+  v[4] = bf_lo(t.z); v[5] = bf_hi(t.z); v[6] = bf_lo(t.w); v[7] = bf_hi(t.w);
+}
+
+__device__ __forceinline__ u32x4_t pack8(const float* v) {
+  return u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                 pack_bf16(v[6], v[7])};
+}
+
+// Eight weights at w + at, or ones.
+__device__ __forceinline__ void load_weights(const float* w, int at, bool active, float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = w != nullptr && active ? w[at + j] : 1.f;
+}
+
+// cos then sin of the row's angles into the wave's own piece of LDS.  LDS
+// operations of one wave run in order, so no barrier is needed; the fences
+// keep the compiler from moving accesses across.
+__device__ __forceinline__ void fill_angles(float (&cs)[2][128], int32_t p, const float* inv_freq,
+                                            int half, int lane) {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  for (int i = lane; i < half; i += 64) {
+    double turn = (double)p * (double)inv_freq[i] * 0.15915494309189534;
+    turn -= rint(turn);
+    float s, c;
+    sincospif(2.f * (float)turn, &s, &c);
+    cs[0][i] = c;
+    cs[1][i] = s;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ void read_angles(const float (&cs)[2][128], int at, bool active,
+                                            float* c, float* s) {
+  const int i = active ? at : 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c[j] = cs[0][i + j];
+    s[j] = cs[1][i + j];
+  }
+}
+
+// inv = 1 / sqrt(sum / hd + eps) of the head held as v[16] by its LPH lanes.
+// Where the sum overflows, or the mean plus eps is below 2^-96, v is scaled by
+// 2^sh (exactly) and inv belongs to the scaled head; sh is 0 elsewhere.
+template <int LPH>
+__device__ __forceinline__ float head_inv_rms(float (&v)[16], float hd, float eps, int& sh) {
+  float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    a0 = __builtin_fmaf(v[j], v[j], a0);
+    a1 = __builtin_fmaf(v[8 + j], v[8 + j], a1);
+  }
+  float T = lanes_sum<LPH>(a0 + a1) / hd + eps;
+  sh = 0;
+  const bool need = T == __builtin_inff() || T < kTiny;
+  if (__builtin_amdgcn_ballot_w64(need) != 0) {      // any head of the wave
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(v[j]));
+    m = lanes_max<LPH>(m);
+    if (need && (m > 0.f || eps > 0.f) && m < __builtin_inff()) sh = rescue_shift(m, eps);
+    a0 = a1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = ldexpf(v[j], sh);
+      v[8 + j] = ldexpf(v[8 + j], sh);
+      a0 = __builtin_fmaf(v[j], v[j], a0);
+      a1 = __builtin_fmaf(v[8 + j], v[8 + j], a1);
+    }
+    const float T2 = lanes_sum<LPH>(a0 + a1) / hd + ldexpf(eps, 2 * sh);
+    if (sh != 0) T = T2;
+  }
+  return inv_sqrt(T);
+}
+
+template <int LPH>
+__global__ void __launch_bounds__(256) qk_rows_rms_kernel(const QkRmsArgs a) {
+  constexpr int HPW = 64 / LPH;
+  __shared__ float trig[kQkRmsRows][2][128];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * kQkRmsRows + wave;
+  if (row >= a.rows) return;
+  const int half = a.hd / 2;
+  const int at = (lane % LPH) * 8;
+  const int hs = lane / LPH;
+  const bool active = at < half;
+  fill_angles(trig[wave], a.pos[row], a.inv_freq, half, lane);
+  float c[8], s[8];
+  read_angles(trig[wave], at, active, c, s);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int nh = a.nh[which];
+    if (nh == 0) continue;
+    float w[16];
+    load_weights(a.w[which], at, active, w);
+    load_weights(a.w[which], half + at, active, w + 8);
+    const uint32_t bytes = (uint32_t)nh * (uint32_t)a.hd * 2u;
+    const RowBuf ib(a.x[which] + row * a.ldx[which], bytes);
+    const RowBuf ob(a.y[which] + row * a.ldy[which], bytes);
+    for (int h0 = 0; h0 < nh; h0 += HPW) {
+      const int lo = active ? ((h0 + hs) * a.hd + at) * 2 : kQkRmsOut;
+      const int hi = active ? lo + a.hd : kQkRmsOut;
+      float v[16];
+      unpack8(ib.ld16(lo), v);
+      unpack8(ib.ld16(hi), v + 8);
+      int sh;
+      const float inv = head_inv_rms<LPH>(v, (float)a.hd, a.eps, sh);
+      float y[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n1 = v[j] * inv * w[j], n2 = v[8 + j] * inv * w[8 + j];
+        y[j] = n1 * c[j] - n2 * s[j];
+        y[8 + j] = n2 * c[j] + n1 * s[j];
+      }
+      ob.st16(pack8(y), lo);
+      ob.st16(pack8(y + 8), hi);
+    }
+  }
+}
+
+// The gradient: the workgroup's four waves walk the rows, each lane summing
+// the weight gradients of its 16 head dimensions over the heads it meets; the
+// workgroup writes one partial sum per dimension.  The number of workgroups,
+// and with it the order of those sums, depends on the row count alone.
+template <int LPH>
+__global__ void __launch_bounds__(256) qk_rows_rms_backward_kernel(const QkRmsArgs a) {
+  constexpr int HPW = 64 / LPH;
+  __shared__ float trig[4][2][128];
+  __shared__ float part[4][2][256];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = a.hd / 2;
+  const int at = (lane % LPH) * 8;
+  const int hs = lane / LPH;
+  const bool active = at < half;
+  const float hd = (float)a.hd;
+  float w[2][16], dw[2][16] = {};
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    load_weights(a.w[which], at, active, w[which]);
+    load_weights(a.w[which], half + at, active, w[which] + 8);
+  }
+  for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < a.rows; row += (int64_t)gridDim.x * 4) {
+    fill_angles(trig[wave], a.pos[row], a.inv_freq, half, lane);
+    float c[8], s[8];
+    read_angles(trig[wave], at, active, c, s);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const int nh = a.nh[which];
+      const uint32_t bytes = (uint32_t)nh * (uint32_t)a.hd * 2u;
+      const RowBuf xb(a.x[which] + row * a.ldx[which], bytes);
+      const RowBuf gb(a.dy[which] + row * a.lddy[which], bytes);
+      const RowBuf ob(a.y[which] + row * a.ldy[which], bytes);
+      for (int h0 = 0; h0 < nh; h0 += HPW) {
+        const int lo = active ? ((h0 + hs) * a.hd + at) * 2 : kQkRmsOut;
+        const int hi = active ? lo + a.hd : kQkRmsOut;
+        float v[16], g[16];
+        unpack8(xb.ld16(lo), v);
+        unpack8(xb.ld16(hi), v + 8);
+        unpack8(gb.ld16(lo), g);
+        unpack8(gb.ld16(hi), g + 8);
+        int sh;
+        const float inv = head_inv_rms<LPH>(v, hd, a.eps, sh);
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d1 = g[j] * c[j] + g[8 + j] * s[j];
+          const float d2 = g[8 + j] * c[j] - g[j] * s[j];
+          v[j] *= inv;                                     // u
+          v[8 + j] *= inv;
+          if ((h0 + hs) < nh) {
+            dw[which][j] = __builtin_fmaf(d1, v[j], dw[which][j]);
+            dw[which][8 + j] = __builtin_fmaf(d2, v[8 + j], dw[which][8 + j]);
+          }
+          g[j] = d1 * w[which][j];
+          g[8 + j] = d2 * w[which][8 + j];
+          a0 = __builtin_fmaf(g[j], v[j], a0);
+          a1 = __builtin_fmaf(g[8 + j], v[8 + j], a1);
+        }
+        const float m = lanes_sum<LPH>(a0 + a1) / hd;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = ldexpf((g[j] - v[j] * m) * inv, sh);
+        ob.st16(pack8(v), lo);
+        ob.st16(pack8(v + 8), hi);
+      }
+    }
+  }
+  if (a.dw_part == nullptr) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float t = dw[which][j];
+      for (int d = LPH; d < 64; d *= 2) t = t + __shfl_xor(t, d);   // heads of the wave step
+      if (hs == 0 && active) part[wave][which][(j < 8 ? 0 : half) + at + j % 8] = t;
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.hd; i += 256) {
+    const int which = i / a.hd, j = i % a.hd;
+    a.dw_part[(int64_t)blockIdx.x * 2 * a.hd + i] =
+        ((part[0][which][j] + part[1][which][j]) + part[2][which][j]) + part[3][which][j];
+  }
+}
+
+// Sums the workgroups' partial weight gradients, in order.
+__global__ void __launch_bounds__(64) qk_rms_weight_sum_kernel(const float* part, int groups,
+                                                               int hd, float* dqw, float* dkw) {
+  const int i = blockIdx.x * 64 + threadIdx.x;
+  if (i >= 2 * hd) return;
+  float t = 0.f;
+  for (int g = 0; g < groups; ++g) t += part[(int64_t)g * 2 * hd + i];
+  float* out = i < hd ? dqw : dkw;
+  if (out != nullptr) out[i % hd] = t;
+}
+
+int qk_rms_backward_groups(int64_t rows) {
+  const int64_t g = (rows + 3) / 4;
+  return (int)(g < 1024 ? g : 1024);
+}
+
+static int lanes_per_head(int hd) {
+  int n = 1;
+  while (n * 16 < hd) n *= 2;
+  return n;
+}
+
+hipError_t launch_qk_rows_rms(const QkRmsArgs& a, int grid, hipStream_t stream) {
+  switch (lanes_per_head(a.hd)) {
+    case 1: qk_rows_rms_kernel<1><<<grid, 256, 0, stream>>>(a); break;
+    case 2: qk_rows_rms_kernel<2><<<grid, 256, 0, stream>>>(a); break;
+    case 4: qk_rows_rms_kernel<4><<<grid, 256, 0, stream>>>(a); break;
+    case 8: qk_rows_rms_kernel<8><<<grid, 256, 0, stream>>>(a); break;
+    case 16: qk_rows_rms_kernel<16><<<grid, 256, 0, stream>>>(a); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_qk_rows_rms_backward(const QkRmsArgs& a, int grid, hipStream_t stream) {
+  switch (lanes_per_head(a.hd)) {
+    case 1: qk_rows_rms_backward_kernel<1><<<grid, 256, 0, stream>>>(a); break;
+    case 2: qk_rows_rms_backward_kernel<2><<<grid, 256, 0, stream>>>(a); break;
+    case 4: qk_rows_rms_backward_kernel<4><<<grid, 256, 0, stream>>>(a); break;
+    case 8: qk_rows_rms_backward_kernel<8><<<grid, 256, 0, stream>>>(a); break;
+    case 16: qk_rows_rms_backward_kernel<16><<<grid, 256, 0, stream>>>(a); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_qk_rms_weight_sum(const float* part, int groups, int hd, float* dqw, float* dkw,
+                                    hipStream_t stream) {
+  qk_rms_weight_sum_kernel<<<(2 * hd + 63) / 64, 64, 0, stream>>>(part, groups, hd, dqw, dkw);
+  return hipGetLastError();
+}
+
+}  // namespace dsr

@@ -1,0 +1,373 @@
+"""ds_logprob_rows and its gradient on the GPU against the float64 oracle.
+
+Bounds, with u = 2^-24.  exp(d) is off by (2 + 2 |d|) u of itself, and
+sum p |d| is below 16 for any row here, so that S = sum exp(d), summed in at
+most 64 steps a chunk and the joins, is off by 128 u; lse and logp add the
+roundings of their own terms.  T = sum exp(d) d likewise, each term by
+(70 + 2 |d|) u.  Gradient: p's exponent costs 2.5 |lp| u, its factors 10 u;
+the oracle states the products these multiply.  A column sum over N rows adds
+N u of its terms.  bf16 outputs add half a bf16 step.
+"""
+import numpy as np
+import pytest
+
+from gpu_util import announce
+from oracle import token_rows as T
+from token_util import U, bf16_round, bits, close, dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from scale_invariant_row_amd import binding
+    binding._token_lib()
+    return binding
+
+
+class Case:
+    def __init__(self, rows, vocab, kind, seed, scaled=True, inv_temp=1.0, masked=0.0, sd=3.0):
+        rng = np.random.default_rng(seed)
+        self.rows, self.vocab, self.kind, self.inv_temp = rows, vocab, kind, inv_temp
+        self.x = (rng.standard_normal((rows, vocab)) * sd).astype(np.float32)
+        if kind == "bf16":
+            self.x = bf16_round(self.x)
+        if masked:
+            self.x[rng.random((rows, vocab)) < masked] = -np.inf
+        self.scale = rng.uniform(0.5, 2, vocab).astype(np.float32) if scaled else None
+        self.labels = rng.integers(0, vocab, rows)
+        if rows > 2:
+            self.labels[1] = -100
+        self.g, self.gh = rng.standard_normal((2, rows)).astype(np.float32)
+
+    @property
+    def z(self):
+        return T.scaled_logits(self.x, self.scale, self.inv_temp)
+
+    def logits(self, pad=0, before=0):
+        """On the device, as a view with `pad` extra columns and `before` elements ahead."""
+        import torch
+        dt = torch.bfloat16 if self.kind == "bf16" else torch.float32
+        ld = self.vocab + pad
+        flat = torch.full((before + self.rows * ld,), float("nan"), dtype=dt, device="cuda:0")
+        v = flat[before:].view(self.rows, ld)[:, :self.vocab]
+        v.copy_(dev(self.x, dt))
+        return v
+
+    def forward(self, B, top_k=0, logits=None, id_type=None):
+        import torch
+        labels = dev(self.labels, id_type or torch.int64)
+        r = B.ds_logprob_rows(self.logits() if logits is None else logits, labels,
+                              None if self.scale is None else dev(self.scale), self.inv_temp, top_k)
+        torch.cuda.synchronize()
+        return r
+
+
+def check(c, r, top_k=0):
+    z = c.z
+    with np.errstate(invalid="ignore"):
+        logp, ent, lse, ids, top = T.logprob_rows(z, c.labels, top_k)
+        m = z.max(-1, keepdims=True).astype(np.float64)
+        d = np.where(z > -np.inf, z - m, 0.0)
+        p = np.where(z > -np.inf, np.exp(np.where(z > -np.inf, z - lse[:, None], -1e3)), 0.0)
+        a1, a2 = (p * np.abs(d)).sum(-1), (p * d * d).sum(-1)
+        known = (c.labels >= 0) & (c.labels < c.vocab)
+        zy = np.where(known, z[np.arange(c.rows), np.where(known, c.labels, 0)], 0.0)
+    fin = lambda v: np.where(np.isfinite(v), np.abs(v), 0.0)  # noqa: E731
+    base = 128 * U + 2 * U * (fin(lse) + fin(m[:, 0]))
+    close(host(r.lse), lse, base, "lse")
+    close(host(r.entropy), ent, 128 * U + U * (fin(ent) + 70 * fin(a1) + 2 * fin(a2)), "entropy")
+    close(host(r.logp), logp, base + 2 * U * (fin(zy) + fin(logp)), "logp")
+    if top_k:
+        assert np.array_equal(host(r.top_ids), ids), "top ids"
+        close(host(r.top_logp), top, base[:, None] + 2 * U * fin(top), "top_logp")
+
+
+SIZES = [(1, 1), (3, 2), (2, 63), (5, 257), (4, 1000), (3, 8191), (3, 8192), (2, 8193), (4, 16387),
+         (2, 50304), (1, 131072)]
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES)
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_forward(B, rows, vocab, kind):
+    c = Case(rows, vocab, kind, rows + vocab, scaled=vocab % 2 == 0, inv_temp=1.0 if rows % 2 else 0.7)
+    k = min(vocab, 7)
+    announce("logprob", rows, vocab, kind)
+    check(c, c.forward(B, k), k)
+
+
+@pytest.mark.parametrize("top_k", [0, 1, 2, 5, 31, 32])
+@pytest.mark.parametrize("vocab", [32, 9000, 40001])
+def test_top_counts(B, top_k, vocab):
+    c = Case(3, vocab, "bf16", top_k + vocab, scaled=False)
+    announce("logprob top", top_k, vocab)
+    check(c, c.forward(B, top_k), top_k)
+
+
+@pytest.mark.parametrize("rows", [7, 300, 1500])
+def test_many_rows(B, rows):
+    c = Case(rows, 9001, "bf16", rows)
+    announce("logprob rows", rows)
+    check(c, c.forward(B, 5), 5)
+
+
+@pytest.mark.parametrize("vocab", [100, 20000, 70001])
+def test_ties_go_to_the_lowest_token(B, vocab):
+    """Few distinct values, so that nearly all of a row ties."""
+    rng = np.random.default_rng(vocab)
+    c = Case(5, vocab, "fp32", vocab, scaled=False)
+    c.x = rng.integers(0, 2, c.x.shape).astype(np.float32)
+    c.x[1] = 0.0                                        # every token the same
+    c.x[2] = np.where(rng.random(vocab) < 0.5, 0.0, -0.0)   # the zeros are equal
+    c.x[3] = -np.inf
+    c.x[3, -3:] = 1.0                                   # ties at the end only
+    c.x[4] = np.arange(vocab)[::-1] // 7                # falling, in sevens
+    announce("logprob ties", vocab)
+    check(c, c.forward(B, 32), 32)
+
+
+def test_rising_and_falling_rows(B):
+    """Every column a new largest value, and the opposite."""
+    c = Case(4, 30000, "fp32", 3, scaled=False)
+    ramp = np.linspace(-20, 20, 30000).astype(np.float32)
+    c.x[:] = ramp, ramp[::-1], np.roll(ramp, 15000), -np.abs(ramp)
+    announce("logprob ramps")
+    check(c, c.forward(B, 20), 20)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_masks(B, kind):
+    """Most tokens masked, all masked, a masked label, fewer tokens than the list."""
+    c = Case(6, 12345, kind, 5, masked=0.9, inv_temp=1.3)
+    c.x[1] = -np.inf
+    c.labels[1] = 3
+    c.x[2] = -np.inf
+    c.x[2, [7, 9000]] = 1.0, 2.0
+    c.labels[2] = 8
+    c.x[3, :8192] = -np.inf                             # a whole chunk
+    c.x[4, 8192:] = -np.inf
+    c.x[5] = -np.inf
+    c.labels[5] = -1
+    announce("logprob masks", kind)
+    r = c.forward(B, 12)
+    check(c, r, 12)
+    assert host(r.logp)[1] == -np.inf and host(r.entropy)[1] == 0 and host(r.lse)[1] == -np.inf
+    assert host(r.top_ids)[2].tolist() == [9000, 7] + [-1] * 10
+    assert host(r.logp)[2] == -np.inf and host(r.logp)[5] == 0
+
+
+def test_lowest_finite_masks_and_large_values(B):
+    """The type's lowest value as a mask, and logits far from zero."""
+    c = Case(4, 9999, "fp32", 6, scaled=False)
+    low = np.finfo(np.float32).min
+    c.x[0, ::2] = low
+    c.x[1] = low                                        # every token at the lowest value: uniform
+    c.x[2] += 30000
+    c.x[3] *= 1000
+    announce("logprob lowest values")
+    r = c.forward(B, 4)
+    check(c, r, 4)
+    assert abs(host(r.entropy)[1] - np.log(9999)) < 1e-5
+
+
+def test_nonfinite(B):
+    c = Case(5, 9000, "fp32", 7, scaled=False)
+    c.x[0, 17] = np.nan
+    c.x[1, 8500] = np.inf
+    c.labels[0] = 4
+    c.x[3] = np.nan
+    announce("logprob non-finite")
+    r = c.forward(B, 3)
+    for got in (r.lse, r.entropy, r.logp):
+        bad = ~np.isfinite(host(got))
+        assert bad[[0, 3]].all() and not bad[[2, 4]].any()
+    assert np.isnan(host(r.lse)[1]) and host(r.top_ids)[1][0] == 8500
+    z = np.where(np.isnan(c.x), -np.inf, c.x)
+    assert host(r.top_ids)[0].tolist() == np.argsort(-z[0], kind="stable")[:3].tolist()
+    assert host(r.top_ids)[3].tolist() == [-1] * 3
+
+
+@pytest.mark.parametrize("kind,pad,before", [("bf16", 3, 0), ("bf16", 1, 5), ("fp32", 5, 0), ("fp32", 1, 3),
+                                             ("bf16", 7, 8), ("bf16", 0, 1)])
+def test_any_row_alignment(B, kind, pad, before):
+    """Rows at any element's address: bits as for aligned rows, NaNs beside
+    the row never read into it."""
+    import torch
+    c = Case(9, 8200 + 5, kind, pad + before)
+    c.g[:] = 1
+    announce("logprob alignment", kind, pad, before)
+    want, got = c.forward(B, 5), c.forward(B, 5, c.logits(pad, before))
+    for a, b in zip(want, got):
+        assert torch.equal(bits(a), bits(b))
+    args = dev(c.labels), want.lse, want.entropy, dev(c.g), dev(c.gh), dev(c.scale)
+    out = c.logits(pad, before)
+    a, da = B.ds_logprob_rows_backward(c.logits(), *args)
+    b, db = B.ds_logprob_rows_backward(c.logits(pad, before), *args, dlogits=out)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(a), bits(b.contiguous())) and torch.equal(bits(da), bits(db))
+
+
+def test_row_bits_do_not_depend_on_the_batch(B):
+    import torch
+    c = Case(700, 20011, "bf16", 9)
+    x, labels, scale = c.logits(), dev(c.labels), dev(c.scale)
+    announce("logprob batch invariance")
+    whole = B.ds_logprob_rows(x, labels, scale, 1.0, 9)
+    for rows in (1, 3, 130):
+        part = B.ds_logprob_rows(x[400:400 + rows], labels[400:400 + rows], scale, 1.0, 9)
+        torch.cuda.synchronize()
+        for a, b in zip(whole, part):
+            assert torch.equal(bits(a[400:400 + rows]), bits(b))
+
+
+def test_outputs_one_at_a_time(B):
+    import torch
+    c = Case(4, 10007, "bf16", 10)
+    announce("logprob without labels, int32 labels")
+    want = c.forward(B, 3)
+    r = B.ds_logprob_rows(c.logits(), None, dev(c.scale))
+    torch.cuda.synchronize()
+    assert r.logp is None and r.top_ids is None
+    assert torch.equal(r.lse, want.lse) and torch.equal(r.entropy, want.entropy)
+    assert torch.equal(c.forward(B, id_type=torch.int32).logp, want.logp)
+    L, x, lse = B._token_lib(), c.logits(), torch.full((6,), 7.0, device="cuda:0")
+    ws = torch.empty(max(16, L.ds_logprob_rows_workspace(4, 10007, 0)), dtype=torch.uint8, device="cuda:0")
+    st = L.ds_logprob_rows(x.data_ptr(), B.DS_TYPE_BF16, 10007, dev(c.scale).data_ptr(), 1.0, None, 8,
+                           None, None, lse.data_ptr() + 4, None, None, 0, 4, 10007, ws.data_ptr(),
+                           ws.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == B.DS_OK and torch.equal(lse[1:5], want.lse) and lse[0] == 7 and lse[5] == 7
+
+
+def backward(B, c, r, g=True, gh=True, **kw):
+    import torch
+    d, ds = B.ds_logprob_rows_backward(
+        kw.pop("logits", None) if "logits" in kw else c.logits(), dev(c.labels), r.lse, r.entropy,
+        dev(c.g) if g else None, dev(c.gh) if gh else None,
+        None if c.scale is None else dev(c.scale), c.inv_temp, **kw)
+    torch.cuda.synchronize()
+    return d, ds
+
+
+def check_backward(c, r, d, ds, g=True, gh=True):
+    dx, dsc, unit, ds_unit, ds_mag = T.logprob_rows_backward(
+        c.x, c.z, c.labels, host(r.lse), host(r.entropy), c.g if g else None, c.gh if gh else None,
+        c.scale, c.inv_temp)
+    close(host(d), dx, 10 * U * unit, "dlogits", bf16=c.kind == "bf16")
+    if ds is not None:
+        close(host(ds), dsc, 10 * U * ds_unit + (c.rows + 4) * U * ds_mag, "dscale")
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES[:-1] + [(70, 3000), (600, 515), (1030, 40)])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_gradient(B, rows, vocab, kind):
+    import torch
+    c = Case(rows, vocab, kind, rows + vocab + 1, scaled=rows != 3, inv_temp=0.8 if rows % 2 else 1.0)
+    announce("logprob gradient", rows, vocab, kind)
+    r = c.forward(B)
+    d, ds = backward(B, c, r)
+    assert (ds is None) == (c.scale is None)
+    check_backward(c, r, d, ds)
+    d2, ds2 = backward(B, c, r)
+    assert torch.equal(bits(d), bits(d2)) and (ds is None or torch.equal(bits(ds), bits(ds2)))
+
+
+@pytest.mark.parametrize("g,gh", [(True, False), (False, True), (False, False)])
+def test_gradient_of_one_output(B, g, gh):
+    c = Case(40, 2049, "fp32", 12)
+    announce("logprob gradient of", g, gh)
+    r = c.forward(B)
+    check_backward(c, r, *backward(B, c, r, g, gh), g, gh)
+
+
+def test_gradient_in_place_and_masked(B):
+    import torch
+    c = Case(20, 9001, "bf16", 13, masked=0.5)
+    c.x[3] = -np.inf
+    announce("logprob gradient in place, masked")
+    r = c.forward(B)
+    want, ds = backward(B, c, r)
+    check_backward(c, r, want, ds)
+    dead = ~np.isfinite(c.x)
+    assert not host(want)[dead].any() and not host(want)[3].any()
+    x = c.logits()
+    got, ds2 = backward(B, c, r, logits=x, dlogits=x)
+    assert got is x and torch.equal(bits(x), bits(want)) and torch.equal(bits(ds), bits(ds2))
+
+
+def test_gradient_leaves_the_padding(B):
+    import torch
+    c = Case(6, 1001, "fp32", 14)
+    r = c.forward(B)
+    buf = torch.full((8, 1010), 5.0, device="cuda:0")
+    announce("logprob gradient into a view")
+    backward(B, c, r, dlogits=buf[1:7, 3:1004])
+    assert (buf[[0, 7]] == 5).all() and (buf[:, :3] == 5).all() and (buf[:, 1004:] == 5).all()
+
+
+def test_gradient_against_differences(B):
+    """Central differences of the kernel's own forward pass along a direction.
+    With steps of 2^-7 the third-order term is h^2 / 6 times the third
+    derivative (at most about 2 |g| + 30 |gh| a row), and the forward's error
+    of some 150 u a row is seen through 2 h."""
+    rng = np.random.default_rng(15)
+    c = Case(30, 700, "fp32", 15, scaled=True, sd=1.0)
+    step = rng.choice([-1.0, 1.0], c.x.shape).astype(np.float32)
+    h = np.float32(2.0 ** -7)
+    announce("logprob gradient against differences")
+    r = c.forward(B)
+    d, ds = backward(B, c, r)
+    x0, s0 = c.x, c.scale
+
+    def loss():
+        f = c.forward(B)
+        return float((host(f.logp).astype(np.float64) * c.g + host(f.entropy).astype(np.float64) * c.gh).sum())
+
+    def along(set_to):
+        set_to(h)
+        hi = loss()
+        set_to(-h)
+        lo = loss()
+        set_to(np.float32(0))
+        return (hi - lo) / (2 * float(h))
+
+    def move_x(t):
+        c.x = x0 + t * step
+
+    def move_s(t):
+        c.scale = s0 + t * step[0]
+
+    size = (np.abs(c.g) * 2 + np.abs(c.gh) * 30).sum()
+    tol = size * float(h) ** 2 * 4 + 150 * U * (np.abs(c.g) + np.abs(c.gh)).sum() * 10 / (2 * float(h))
+    assert abs(along(move_x) - (host(d) * step).sum()) <= tol
+    assert abs(along(move_s) - (host(ds) * step[0]).sum()) <= 4 * tol     # logits of a few units
+
+
+def test_offsets_past_32_bits(B):
+    """Rows that start past 4 GiB: a strided view whose last rows lie there."""
+    import torch
+    vocab, ld, rows = 1003, 1 << 20, 2100                   # 4.4 GB of bf16 between first and last
+    announce("logprob rows past 4 GiB")
+    buf = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda:0")
+    x = buf.view(rows, ld)[:, :vocab]
+    g = torch.Generator(device="cuda:0").manual_seed(3)
+    x.copy_(torch.randn(rows, vocab, device="cuda:0", generator=g))
+    small = x.contiguous()
+    labels = torch.randint(0, vocab, (rows,), device="cuda:0", generator=g)
+    ones = torch.ones(rows, device="cuda:0")
+    a, b = (B.ds_logprob_rows(t, labels, top_k=4) for t in (x, small))
+    da, db = (B.ds_logprob_rows_backward(t, labels, a.lse, a.entropy, ones, ones)[0] for t in (x, small))
+    torch.cuda.synchronize()
+    for s, t in zip(a, b):
+        assert torch.equal(bits(s), bits(t))
+    assert torch.equal(bits(da), bits(db))
+
+
+def test_no_rows(B):
+    import torch
+    c = Case(0, 100, "bf16", 16)
+    announce("logprob of no rows")
+    r = c.forward(B, 3)
+    d, ds = backward(B, c, r)
+    assert r.logp.shape == (0,) and r.top_ids.shape == (0, 3) and d.shape == (0, 100)
+    assert not ds.any()
