@@ -180,7 +180,7 @@ int64_t ds_qk_rows_rms_backward_workspace(int64_t rows, int32_t n_q_heads, int32
  * top_k    : 0 <= top_k <= min(DS_MAX_TOP, vocab).
  * vocab    : 1 <= vocab <= DS_MAX_VOCAB.  rows >= 0 (0: no-op).
  *
- * A logit of -infinity is a masked token: probability 0, logp -infinity,
+ * A token with z = -infinity is masked: probability 0, logp -infinity,
  * never listed.  A list with fewer than top_k unmasked tokens ends in id -1
  * and log probability -infinity.  A row with every token masked has lse
  * -infinity, entropy 0 and logp -infinity (0 if ignored).  A row holding a

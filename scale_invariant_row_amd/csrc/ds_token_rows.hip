@@ -358,7 +358,7 @@ int64_t ds_logprob_rows_workspace(int64_t rows, int64_t vocab, int32_t top_k) {
   int st = check_logits(DS_TYPE_F32, vocab, 1.f, 8, rows, vocab);
   if (st != DS_OK) return st;
   if (top_k < 0 || top_k > DS_MAX_TOP || top_k > vocab) return DS_ERR_SHAPE;
-  return 0;
+  return dsr::logprob_workspace(rows, vocab, top_k);
 }
 
 int ds_logprob_rows(const void* logits, int32_t logits_type, int64_t ld, const float* scale,
@@ -411,7 +411,7 @@ int ds_logprob_rows(const void* logits, int32_t logits_type, int64_t ld, const f
 int64_t ds_logprob_rows_backward_workspace(int64_t rows, int64_t vocab) {
   int st = check_logits(DS_TYPE_F32, vocab, 1.f, 8, rows, vocab);
   if (st != DS_OK) return st;
-  return 0;
+  return dsr::logprob_grad_workspace(rows, vocab);
 }
 
 int ds_logprob_rows_backward(const void* logits, int32_t logits_type, int64_t ld,

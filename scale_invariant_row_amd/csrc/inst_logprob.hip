@@ -5,21 +5,35 @@
 //   entropy = lse - sum p z = log S - T / S  with  M = max z,
 //             S = sum exp(z - M),  T = sum exp(z - M) (z - M)
 //
-// The row is cut into chunks of kLpChunk columns.  A chunk's (M, S, T) comes
-// from its own maximum; the chunks are joined left to right (lp_join), so the
-// row's bits depend on the row and its width alone.
+// The row is cut into chunks of kLpChunk columns.  One wave holds a chunk in
+// registers (32 values a lane, read once), takes its maximum, and then its S
+// and T about that maximum, so no exponential is ever rescaled inside a
+// chunk.  The chunks' (M, S, T) are joined by a tree that the number of chunks
+// fixes, whoever computed them: the row's bits depend on the row and its width
+// alone, and a row may be spread over any number of waves.
 //
-// exp(-inf) = 0 lets a masked token (z = -inf) drop out of S; in T it would
-// be 0 * inf, so the factor z - M is clamped at -200, where exp is 0 already.
+// Cost per value beside its load: unpack, scale, half a maximum, one fused
+// multiply-add to log2 units, exp2 (four issue slots), a sum and a fused
+// multiply-add: 10 slots, 270 us for 8,192 x 131,072 bf16 values, under the
+// time their 2.1 GB take from memory.
+//
+// Masked tokens (z = -inf) have exp 0 but 0 * -inf in T.  The fast sums go
+// without a test for them: a chunk whose sums come out NaN, or that holds
+// nothing above -inf, is summed again in the careful form (lp_careful), where
+// the factor is clamped at -200 (exp is 0 there already); a NaN of the row's
+// own stays NaN.
+#include <algorithm>
+#include <type_traits>
+
 #include "row_kernels.hpp"
 #include "token_launch.hpp"
 
 namespace dsr {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpPer = 32;                            // columns per thread of a chunk
-constexpr int kLpChunk = kLpThreads * kLpPer;         // 8,192
+constexpr int kLpPer = 32;                            // columns per lane of a chunk
+constexpr int kLpChunk = 64 * kLpPer;                 // 2,048
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float lp_exp(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
@@ -46,8 +60,8 @@ struct LpSum {
   float M, S, T;
 };
 
-// Joins the sums of a stretch with those of the stretch to its right.  With
-// every token masked so far, M is -inf and S, T are 0.
+// Joins the sums of two stretches.  With every token of a stretch masked, M
+// is -inf and S, T are 0.
 __device__ __forceinline__ LpSum lp_join(LpSum a, LpSum b) {
   const float M = fmaxf(a.M, b.M);
   const float base = M == -__builtin_inff() ? 0.f : M;
@@ -60,117 +74,416 @@ __device__ __forceinline__ LpSum lp_join(LpSum a, LpSum b) {
   return r;
 }
 
-// A key that orders tokens: larger z first, then the lower column.  0 for a
-// token that cannot be listed (masked, or NaN).
-__device__ __forceinline__ uint64_t lp_key(float z, int col) {
-  if (!(z > -__builtin_inff())) return 0;
-  const uint32_t u = __float_as_uint(z + 0.f);        // -0 orders as 0
-  const uint32_t k = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-  return ((uint64_t)k << 32) | (uint32_t)~(uint32_t)col;
+// The joined sums of n chunks, in every lane: lane l takes chunks l, l + 64,
+// ... in order, then the lanes pair up.  get(c) gives chunk c's sums.
+template <class F>
+__device__ __forceinline__ LpSum lp_join_all(int n, int lane, F&& get) {
+  LpSum s = {-__builtin_inff(), 0.f, 0.f};
+  for (int c = lane; c < n; c += 64) s = lp_join(s, get(c));
+  for (int d = 1; d < 64; d *= 2) {
+    const LpSum o = {__shfl_xor(s.M, d), __shfl_xor(s.S, d), __shfl_xor(s.T, d)};
+    s = lp_join(s, o);
+  }
+  return s;
 }
 
-__device__ __forceinline__ float lp_key_z(uint64_t key) {
-  const uint32_t k = (uint32_t)(key >> 32);
+// -------------------------------------------------------- top alternatives
+//
+// A key orders tokens: larger z first, then the lower column.  0 stands for a
+// token that cannot be listed (masked, or NaN).  A wave keeps its best tokens
+// as a sorted list over its lanes (lane i the i-th best); a chunk's values
+// are looked at one by one only where a lane's maximum beats the list's k-th.
+
+__device__ __forceinline__ uint32_t lp_order(float z) {
+  const uint32_t u = __float_as_uint(z + 0.f);        // -0 orders as 0
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float lp_unorder(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-__device__ __forceinline__ uint64_t lp_wave_max(uint64_t v) {
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t o = __shfl_xor((unsigned long long)v, d);
-    v = o > v ? o : v;
-  }
-  return v;
+__device__ __forceinline__ uint64_t lp_key(float z, int col) {
+  return z > -__builtin_inff() ? ((uint64_t)lp_order(z) << 32) | (uint32_t)~(uint32_t)col : 0;
 }
 
+__device__ __forceinline__ uint64_t lp_read_lane(uint64_t v, int lane) {
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// v of the lane below (lane 0 keeps its own).
+__device__ __forceinline__ uint64_t lp_lane_below(uint64_t v) {
+  const int hi = (int)(v >> 32), lo = (int)(uint32_t)v;
+  const uint32_t h = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, 0x138, 0xF, 0xF, false);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, 0x138, 0xF, 0xF, false);
+  return ((uint64_t)h << 32) | l;
+}
+
+struct LpTop {
+  uint64_t key = 0;        // lane i: the i-th best so far, 0 past the end
+  uint64_t kth = 0;        // the k-th best (uniform)
+
+  // One key (uniform) into its place.
+  __device__ __forceinline__ void insert(uint64_t k, int top_k, int lane) {
+    const int pos = __builtin_popcountll(__builtin_amdgcn_ballot_w64(key > k));
+    const uint64_t below = lp_lane_below(key);
+    key = lane < pos ? key : lane == pos ? k : below;
+    kth = lp_read_lane(key, top_k - 1);
+  }
+
+  // Every lane's key that belongs in the list, lowest lane first.
+  __device__ __forceinline__ void add(uint64_t k, int top_k, int lane) {
+    uint64_t hits = __builtin_amdgcn_ballot_w64(k > kth);
+    while (hits != 0) {
+      const int l = __builtin_ctzll(hits);
+      insert(lp_read_lane(k, l), top_k, lane);
+      hits &= __builtin_amdgcn_ballot_w64(k > kth);
+      hits &= ~(1ull << l);
+    }
+  }
+};
+
+// A lower bound of the k-th largest of the lanes' values (in lp_order's
+// order): its upper 16 bits, found bit by bit.  At least k lanes reach it.
+__device__ __forceinline__ uint32_t lp_kth_lane(uint32_t u, int k) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int b = 31; b >= 16; --b) {
+    const uint32_t c = t | (1u << b);
+    if (__builtin_popcountll(__builtin_amdgcn_ballot_w64(u >= c)) >= k) t = c;
+  }
+  return t;
+}
+
+// ------------------------------------------------------------ chunk of a row
+//
+// Lane l holds, of each stretch of 64 vectors, the l-th: 8 bf16 or 4 fp32
+// columns, 16 bytes, at whatever alignment the row has (global loads need
+// none beyond the element's).
+
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
+typedef f32x4_t f32x4_a4 __attribute__((aligned(4)));
+
 template <bool F32>
-__global__ void __launch_bounds__(kLpThreads) logprob_rows_kernel(const LogprobArgs a) {
-  __shared__ float red[4][2];
-  __shared__ uint64_t kred[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = blockIdx.x;
-  const int64_t at = row * a.ld;
-  LpSum sum = {-__builtin_inff(), 0.f, 0.f};
-  for (int c0 = 0; c0 < a.vocab; c0 += kLpChunk) {
+struct LpRaw {
+  static constexpr int VE = F32 ? 4 : 8;              // columns per vector
+  static constexpr int NV = kLpPer / VE;
+  u32x4_t r[NV];
+
+  static __device__ __forceinline__ int col(int c0, int v, int lane) {
+    return c0 + (v * 64 + lane) * VE;
+  }
+
+  // The chunk at column c0; columns past the row read as -inf.
+  __device__ __forceinline__ void load(const void* x, int64_t at, int c0, int vocab, int lane) {
+    using V = typename std::conditional<F32, u32x4_a4, u32x4_a2>::type;
+    using E = typename std::conditional<F32, uint32_t, uint16_t>::type;
+    const E* row = static_cast<const E*>(x) + at;
+    if (c0 + kLpChunk <= vocab) {                     // uniform
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        r[v] = __builtin_nontemporal_load(reinterpret_cast<const V*>(row + col(c0, v, lane)));
+      return;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = col(c0, v, lane);
+      if (c + VE <= vocab) {
+        r[v] = *reinterpret_cast<const V*>(row + c);
+      } else {
+        uint32_t e[VE];
+#pragma unroll
+        for (int k = 0; k < VE; ++k)
+          e[k] = c + k < vocab ? (uint32_t)row[c + k] : F32 ? 0xff800000u : 0xff80u;
+        if constexpr (F32) r[v] = u32x4_t{e[0], e[1], e[2], e[3]};
+        else r[v] = u32x4_t{e[0] | e[1] << 16, e[2] | e[3] << 16, e[VE - 4] | e[VE - 3] << 16,
+                            e[VE - 2] | e[VE - 1] << 16};
+      }
+    }
+  }
+
+  __device__ __forceinline__ float at(int i) const {  // i-th of the lane's 32 values
+    const u32x4_t t = r[i / VE];
+    const int w = i % VE;
+    if constexpr (F32) return __uint_as_float(t[w]);
+    else return w % 2 == 0 ? bf_lo(t[w / 2]) : bf_hi(t[w / 2]);
+  }
+};
+
+// The scale of a lane's 32 columns (1 past the row).
+template <bool F32>
+__device__ __forceinline__ void lp_load_scale(float (&sc)[kLpPer], const float* scale, int c0,
+                                              int vocab, int lane) {
+  using R = LpRaw<F32>;
+  const bool whole = c0 + kLpChunk <= vocab;
+#pragma unroll
+  for (int v = 0; v < R::NV; ++v) {
+    const int c = R::col(c0, v, lane);
+    if (whole || c + R::VE <= vocab) {
+#pragma unroll
+      for (int h = 0; h < R::VE; h += 4) {
+        const f32x4_t t = *reinterpret_cast<const f32x4_a4*>(scale + c + h);
+        sc[v * R::VE + h] = t.x; sc[v * R::VE + h + 1] = t.y;
+        sc[v * R::VE + h + 2] = t.z; sc[v * R::VE + h + 3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < R::VE; ++k) sc[v * R::VE + k] = c + k < vocab ? scale[c + k] : 1.f;
+    }
+  }
+}
+
+// S and T about base with every step guarded: see the head of this file.
+__device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float M) {
+  const float base = M == -__builtin_inff() ? 0.f : M;
+  float S = 0.f, T = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLpPer; ++i) {
+    const float d = z[i] - base, e = lp_exp(d);
+    S += e;
+    T = __builtin_fmaf(e, fmaxf(d, -200.f), T);
+  }
+  return LpSum{M, wave_sum(S), wave_sum(T)};
+}
+
+// A chunk's sums, the same in every lane.  With c = fp32(M log2 e) the fast
+// form sums about c in log2 units, z log2 e - c one fused multiply-add; r, the
+// rounding error of c (a fused multiply-add gives it exactly), turns the sums
+// into those about M:  z log2 e - c = (z - M) log2 e + r.
+__device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float M) {
+  const float c = M * kLog2e;
+  float S = 0.f, T = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLpPer; ++i) {
+    const float d = __builtin_fmaf(z[i], kLog2e, -c), e = __builtin_amdgcn_exp2f(d);
+    S += e;
+    T = __builtin_fmaf(e, d, T);
+  }
+  S = wave_sum(S);
+  T = wave_sum(T);
+  if (!(S < __builtin_inff() && T == T)) return lp_careful(z, M);      // uniform
+  const float r = __builtin_fmaf(M, kLog2e, -c);
+  const float f = __builtin_amdgcn_exp2f(-r);
+  return LpSum{M, S * f, (T - r * S) * f * kLn2};
+}
+
+// Row r of a workgroup's rows, one of `waves` waves that share them: the
+// chunks first, first + waves, ...
+template <bool F32, bool SCALED>
+struct LpRow {
+  LpTop top;
+
+  __device__ __forceinline__ LpSum chunk(const LpRaw<F32>& raw, const float (&sc)[kLpPer],
+                                         float inv_temp, int c0, int top_k, int lane) {
+    using R = LpRaw<F32>;
     float z[kLpPer];
     float m = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < kLpPer; ++i) {
-      const int col = c0 + i * kLpThreads + threadIdx.x;
-      z[i] = col < a.vocab ? lp_z(lp_load<F32>(a.x, at + col), a.scale, col, a.inv_temp)
-                           : -__builtin_inff();
-      m = fmaxf(m, z[i]);
+      z[i] = raw.at(i);
+      if constexpr (SCALED) z[i] = z[i] * sc[i];
     }
-    m = wave_max(m);
-    __syncthreads();
-    if (lane == 0) red[wave][0] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-    const float base = m == -__builtin_inff() ? 0.f : m;
-    float S = 0.f, T = 0.f;
+    if (inv_temp != 1.f) {                            // uniform; * 1 changes nothing
 #pragma unroll
-    for (int i = 0; i < kLpPer; ++i) {
-      const float d = z[i] - base, e = lp_exp(d);
-      S += e;
-      T = __builtin_fmaf(e, fmaxf(d, -200.f), T);
+      for (int i = 0; i < kLpPer; ++i) z[i] = z[i] * inv_temp;
     }
-    S = wave_sum(S);
-    T = wave_sum(T);
-    __syncthreads();
-    if (lane == 0) {
-      red[wave][0] = S;
-      red[wave][1] = T;
+#pragma unroll
+    for (int i = 0; i < kLpPer; ++i) m = fmaxf(m, z[i]);
+    const LpSum s = lp_chunk_sum(z, wave_max(m));
+    if (top_k > 0) {
+      const float kz = top.kth != 0 ? lp_unorder((uint32_t)(top.kth >> 32)) : -__builtin_inff();
+      const uint64_t hits = __builtin_amdgcn_ballot_w64(m > kz);
+      if (hits != 0) {
+        // many lanes: only values that reach the k-th largest lane maximum
+        // can be among the chunk's k best
+        float least = -__builtin_inff();
+        if (__builtin_popcountll(hits) > top_k) {
+          const uint32_t t = lp_kth_lane(m > -__builtin_inff() ? lp_order(m) : 0u, top_k);
+          if (t != 0) least = lp_unorder(t);
+        }
+#pragma unroll
+        for (int i = 0; i < kLpPer; ++i) {
+          const bool may = z[i] > kz && z[i] >= least;
+          if (__builtin_amdgcn_ballot_w64(may) != 0)
+            top.add(may ? lp_key(z[i], R::col(c0, i / R::VE, lane) + i % R::VE) : 0, top_k, lane);
+        }
+      }
     }
-    __syncthreads();
-    const LpSum c = {m, ((red[0][0] + red[1][0]) + red[2][0]) + red[3][0],
-                     ((red[0][1] + red[1][1]) + red[2][1]) + red[3][1]};
-    sum = lp_join(sum, c);
+    return s;
   }
+};
+
+// Writes a row's three numbers and its list from the joined sums; zy is the
+// label's z (read ahead), y its column or -1.
+__device__ __forceinline__ void lp_write_row(const LogprobArgs& a, int64_t row, LpSum sum,
+                                             uint64_t key, int y, float zy, int lane) {
   const bool empty = sum.M == -__builtin_inff() && sum.S == 0.f;
   const float log_s = logf(sum.S);
-  const float lse = empty ? -__builtin_inff() : sum.M + log_s;
-  if (threadIdx.x == 0) {
-    if (a.lse != nullptr) a.lse[row] = lse;
+  if (lane == 0) {
+    if (a.lse != nullptr) a.lse[row] = empty ? -__builtin_inff() : sum.M + log_s;
     if (a.entropy != nullptr) a.entropy[row] = empty ? 0.f : log_s - sum.T / sum.S;
-    if (a.logp != nullptr) {
-      const int y = lp_label(a.labels, a.label_bytes, row, a.vocab);
-      float lp = 0.f;
-      if (y >= 0) {
-        const float z = lp_z(lp_load<F32>(a.x, at + y), a.scale, y, a.inv_temp);
-        lp = empty ? -__builtin_inff() : (z - sum.M) - log_s;
-      }
-      a.logp[row] = lp;
-    }
+    if (a.logp != nullptr)
+      a.logp[row] = y < 0 ? 0.f : empty ? -__builtin_inff() : (zy - sum.M) - log_s;
   }
-  // the top alternatives, one pass over the row for each: the largest key
-  // below the last
-  uint64_t last = ~0ull;
-  for (int k = 0; k < a.top_k; ++k) {
-    uint64_t best = 0;
-    for (int col = threadIdx.x; col < a.vocab; col += kLpThreads) {
-      const uint64_t key = lp_key(lp_z(lp_load<F32>(a.x, at + col), a.scale, col, a.inv_temp), col);
-      if (key < last && key > best) best = key;
-    }
-    best = lp_wave_max(best);
-    __syncthreads();
-    if (lane == 0) kred[wave] = best;
-    __syncthreads();
-    for (int w = 0; w < 4; ++w) best = kred[w] > best ? kred[w] : best;
-    last = best;
-    if (threadIdx.x == 0) {
-      a.top_ids[row * a.top_k + k] = best != 0 ? (int32_t)~(uint32_t)best : -1;
-      a.top_logp[row * a.top_k + k] = best != 0 ? (lp_key_z(best) - sum.M) - log_s : -__builtin_inff();
-    }
+  if (lane < a.top_k) {
+    a.top_ids[row * a.top_k + lane] = key != 0 ? (int32_t)~(uint32_t)key : -1;
+    a.top_logp[row * a.top_k + lane] =
+        key != 0 ? (lp_unorder((uint32_t)(key >> 32)) - sum.M) - log_s : -__builtin_inff();
   }
 }
 
-hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace,
-                               hipStream_t stream) {
-  (void)workspace;
-  constexpr int64_t kMostRows = 1 << 20;               // rows per launch
+// One workgroup of four waves per ROWS rows.  Each wave takes every fourth
+// chunk of all of them, so a chunk's scale is loaded once for ROWS rows; the
+// next row's values are on their way while one is summed.  Dynamic LDS: the
+// chunks' sums, [ROWS][chunks].
+template <bool F32, bool SCALED, int ROWS>
+__global__ void __launch_bounds__(256) logprob_rows_kernel(const LogprobArgs a, int chunks) {
+  extern __shared__ float sums[];
+  __shared__ uint64_t lists[ROWS][4][32];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = (int64_t)blockIdx.x * ROWS;
+  const int rows = (int)(a.rows - row0 < ROWS ? a.rows - row0 : ROWS);
+  // wave r writes row r: its label's z on the way
+  int y = -1;
+  float zy = 0.f;
+  if (wave < rows) {
+    y = lp_label(a.labels, a.label_bytes, row0 + wave, a.vocab);
+    if (y >= 0) zy = lp_z(lp_load<F32>(a.x, (row0 + wave) * a.ld + y), a.scale, y, a.inv_temp);
+  }
+  LpRow<F32, SCALED> st[ROWS];
+  LpRaw<F32> raw;
+  if (wave < chunks) raw.load(a.x, row0 * a.ld, wave * kLpChunk, a.vocab, lane);
+  for (int c = wave; c < chunks; c += 4) {
+    float sc[kLpPer];
+    if constexpr (SCALED) lp_load_scale<F32>(sc, a.scale, c * kLpChunk, a.vocab, lane);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (r >= rows) break;                           // uniform
+      const LpRaw<F32> now = raw;
+      const bool last = r + 1 >= rows;
+      const int nc = last ? c + 4 : c;
+      if (nc < chunks)
+        raw.load(a.x, (row0 + (last ? 0 : r + 1)) * a.ld, nc * kLpChunk, a.vocab, lane);
+      const LpSum s = st[r].chunk(now, sc, a.inv_temp, c * kLpChunk, a.top_k, lane);
+      if (lane == 0) {
+        float* p = sums + ((int64_t)r * chunks + c) * 3;
+        p[0] = s.M; p[1] = s.S; p[2] = s.T;
+      }
+    }
+  }
+  if (a.top_k > 0 && lane < a.top_k) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) lists[r][wave][lane] = st[r].top.key;
+  }
+  __syncthreads();
+  if (wave >= rows) return;
+  const LpSum sum = lp_join_all(chunks, lane, [&](int c) {
+    const float* p = sums + ((int64_t)wave * chunks + c) * 3;
+    return LpSum{p[0], p[1], p[2]};
+  });
+  LpTop top;
+  if (a.top_k > 0) {
+    const bool in = lane < a.top_k;
+    top.key = in ? lists[wave][0][lane] : 0;
+    top.kth = lp_read_lane(top.key, a.top_k - 1);
+    for (int w = 1; w < 4; ++w) top.add(in ? lists[wave][w][lane] : 0, a.top_k, lane);
+  }
+  lp_write_row(a, row0 + wave, sum, top.key, y, zy, lane);
+}
+
+// Few rows: a row is spread over `splits` workgroups; wave w of the row's
+// 4 splits takes chunks w, w + 4 splits, ...  The chunks' sums and the waves'
+// lists go to the workspace, sums [rows][chunks][3], then keys
+// [rows][top_k][waves].
+template <bool F32, bool SCALED>
+__global__ void __launch_bounds__(256)
+logprob_split_kernel(const LogprobArgs a, int chunks, int splits, float* sums, uint64_t* keys) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = blockIdx.x / splits;
+  const int waves = splits * 4;
+  const int w = (int)(blockIdx.x % splits) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  LpRow<F32, SCALED> st;
+  for (int c = w; c < chunks; c += waves) {
+    LpRaw<F32> raw;
+    float sc[kLpPer];
+    raw.load(a.x, row * a.ld, c * kLpChunk, a.vocab, lane);
+    if constexpr (SCALED) lp_load_scale<F32>(sc, a.scale, c * kLpChunk, a.vocab, lane);
+    const LpSum s = st.chunk(raw, sc, a.inv_temp, c * kLpChunk, a.top_k, lane);
+    if (lane == 0) {
+      float* p = sums + (row * chunks + c) * 3;
+      p[0] = s.M; p[1] = s.S; p[2] = s.T;
+    }
+  }
+  if (lane < a.top_k) keys[(row * a.top_k + lane) * waves + w] = st.top.key;
+}
+
+// Joins a split row: one wave per row.  The lists are sorted, so once no wave
+// has a place-j key for the list, deeper ones have none either.
+template <bool F32>
+__global__ void __launch_bounds__(64)
+logprob_join_kernel(const LogprobArgs a, int chunks, int waves, const float* sums,
+                    const uint64_t* keys) {
+  const int lane = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const int y = lp_label(a.labels, a.label_bytes, row, a.vocab);
+  const float zy = y >= 0 ? lp_z(lp_load<F32>(a.x, row * a.ld + y), a.scale, y, a.inv_temp) : 0.f;
+  const LpSum sum = lp_join_all(chunks, lane, [&](int c) {
+    const float* p = sums + (row * chunks + c) * 3;
+    return LpSum{p[0], p[1], p[2]};
+  });
+  LpTop top;
+  for (int j = 0; j < a.top_k; ++j) {
+    uint64_t any = 0;
+    for (int w0 = 0; w0 < waves; w0 += 64) {
+      const uint64_t k = w0 + lane < waves ? keys[(row * a.top_k + j) * waves + w0 + lane] : 0;
+      any |= __builtin_amdgcn_ballot_w64(k > top.kth);
+      top.add(k, a.top_k, lane);
+    }
+    if (any == 0) break;
+  }
+  lp_write_row(a, row, sum, top.key, y, zy, lane);
+}
+
+static int lp_chunks(int64_t vocab) { return (int)((vocab + kLpChunk - 1) / kLpChunk); }
+
+// Workgroups a row is spread over: enough for about 2,048 waves in all (two
+// for each SIMD), as far as it has chunks.  Results do not depend on it.
+static int lp_splits(int64_t rows, int chunks) {
+  const int64_t want = (512 + rows - 1) / (rows > 0 ? rows : 1);
+  const int most = (chunks + 3) / 4;
+  return (int)(want < most ? want : most);
+}
+
+int64_t logprob_workspace(int64_t rows, int64_t vocab, int top_k) {
+  const int chunks = lp_chunks(vocab), splits = lp_splits(rows, chunks);
+  if (rows == 0 || splits <= 1) return 0;
+  const int64_t sums = (rows * chunks * 12 + 15) / 16 * 16;
+  return sums + rows * top_k * splits * 4 * 8;
+}
+
+template <bool F32, bool SCALED>
+static hipError_t run_logprob(const LogprobArgs& a, void* workspace, hipStream_t stream) {
+  const int chunks = lp_chunks(a.vocab), splits = lp_splits(a.rows, chunks);
+  if (splits > 1) {                                   // at most 511 rows
+    float* sums = static_cast<float*>(workspace);
+    auto* keys = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) +
+                                             (a.rows * chunks * 12 + 15) / 16 * 16);
+    logprob_split_kernel<F32, SCALED>
+        <<<(int)a.rows * splits, 256, 0, stream>>>(a, chunks, splits, sums, keys);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    logprob_join_kernel<F32><<<(int)a.rows, 64, 0, stream>>>(a, chunks, splits * 4, sums, keys);
+    return hipGetLastError();
+  }
+  constexpr int64_t kMostRows = 1 << 20;              // rows per launch
   for (int64_t r0 = 0; r0 < a.rows; r0 += kMostRows) {
     LogprobArgs p = a;
-    const int64_t n = a.rows - r0 < kMostRows ? a.rows - r0 : kMostRows;
-    p.x = static_cast<const char*>(a.x) + r0 * a.ld * (f32 ? 4 : 2);
+    p.rows = a.rows - r0 < kMostRows ? a.rows - r0 : kMostRows;
+    p.x = static_cast<const char*>(a.x) + r0 * a.ld * (F32 ? 4 : 2);
     if (a.labels != nullptr) p.labels = static_cast<const char*>(a.labels) + r0 * a.label_bytes;
     if (a.logp != nullptr) p.logp = a.logp + r0;
     if (a.entropy != nullptr) p.entropy = a.entropy + r0;
@@ -179,17 +492,46 @@ hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace,
       p.top_ids = a.top_ids + r0 * a.top_k;
       p.top_logp = a.top_logp + r0 * a.top_k;
     }
-    if (f32) logprob_rows_kernel<true><<<(int)n, kLpThreads, 0, stream>>>(p);
-    else logprob_rows_kernel<false><<<(int)n, kLpThreads, 0, stream>>>(p);
+    // four rows a workgroup share each load of the scale, once there are
+    // workgroups enough
+    const bool many = SCALED && a.rows >= 4096;
+    if constexpr (SCALED) {
+      if (many)
+        logprob_rows_kernel<F32, true, 4>
+            <<<(int)((p.rows + 3) / 4), 256, (size_t)4 * chunks * 12, stream>>>(p, chunks);
+    }
+    if (!many)
+      logprob_rows_kernel<F32, SCALED, 1><<<(int)p.rows, 256, (size_t)chunks * 12, stream>>>(p, chunks);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-// What the gradient needs of a row.
+hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace,
+                               hipStream_t stream) {
+  if (f32)
+    return a.scale != nullptr ? run_logprob<true, true>(a, workspace, stream)
+                              : run_logprob<true, false>(a, workspace, stream);
+  return a.scale != nullptr ? run_logprob<false, true>(a, workspace, stream)
+                            : run_logprob<false, false>(a, workspace, stream);
+}
+
+// ------------------------------------------------------------- the gradient
+//
+//   dz = tau (dlogp [j = label] - p (dlogp + dentropy (log p + entropy)))
+//
+// Given lse, every element stands by itself.  A workgroup takes a strip of
+// columns (16 bytes a thread) down a tile of rows, so a column's scale is
+// loaded, and its gradient summed, once per tile; the tiles' sums go to the
+// workspace and are added in order by a second kernel.  What a row needs is
+// folded into five numbers in LDS:  d = p (gh lp + c), lp = z - lse.
+//
+// lp is clamped at -200, where p is 0, so that a masked token's 0 * inf does
+// not arise; c is NaN where lse is, so that row's NaN is kept.
+
 struct LpRowGrad {
-  float lse, ent, g, gh;       // g: dlogp (0 for an ignored row), gh: dentropy
+  float lse, gh, c, hot;       // hot: tau dlogp, added at the label
   int label;
 };
 
@@ -197,77 +539,190 @@ __device__ __forceinline__ LpRowGrad lp_row_grad(const LogprobGradArgs& a, int64
   LpRowGrad r;
   r.label = lp_label(a.labels, a.label_bytes, row, a.vocab);
   r.lse = a.lse[row];
-  r.ent = a.dentropy != nullptr ? a.entropy[row] : 0.f;
-  r.g = a.dlogp != nullptr && r.label >= 0 ? a.dlogp[row] : 0.f;
-  r.gh = a.dentropy != nullptr ? a.dentropy[row] : 0.f;
+  const float g = a.dlogp != nullptr && r.label >= 0 ? a.dlogp[row] * a.inv_temp : 0.f;
+  const float h = a.dentropy != nullptr ? a.dentropy[row] * a.inv_temp : 0.f;
+  r.gh = -h;
+  r.c = a.dentropy != nullptr ? -__builtin_fmaf(h, a.entropy[row], g) : -g;
+  r.hot = g;
+  if (r.lse != r.lse) r.c = r.lse;
+  if (r.lse == -__builtin_inff()) {                   // every token masked: no gradient
+    r.lse = __builtin_inff();
+    r.hot = 0.f;
+  }
   return r;
 }
 
-// dz_j inv_temp; 0 for a masked token (and so for a row with all masked).
-__device__ __forceinline__ float lp_dz(const LpRowGrad& r, float z, int col, float inv_temp) {
-  const float lp = z - r.lse;
-  const float p = lp_exp(lp);
-  float d = r.gh * (lp + r.ent) + r.g;
-  d = (col == r.label ? r.g : 0.f) - p * d;
-  return z == -__builtin_inff() ? 0.f : d * inv_temp;
-}
+constexpr int kLpTileRows = 128;                      // most rows of a tile
 
 template <bool F32>
-__global__ void __launch_bounds__(kLpThreads) logprob_grad_kernel(const LogprobGradArgs a) {
-  const int64_t row = blockIdx.x;
-  const LpRowGrad r = lp_row_grad(a, row);
-  for (int col = threadIdx.x; col < a.vocab; col += kLpThreads) {
-    const float z = lp_z(lp_load<F32>(a.x, row * a.ld + col), a.scale, col, a.inv_temp);
-    float d = lp_dz(r, z, col, a.inv_temp);
-    if (a.scale != nullptr) d = d * a.scale[col];
-    if constexpr (F32) static_cast<float*>(a.dx)[row * a.ldo + col] = d;
-    else static_cast<uint16_t*>(a.dx)[row * a.ldo + col] = (uint16_t)pack_bf16(d, 0.f);
+struct LpVec {                                        // a thread's 16 bytes
+  static constexpr int VE = F32 ? 4 : 8;
+  using V = typename std::conditional<F32, u32x4_a4, u32x4_a2>::type;
+  using E = typename std::conditional<F32, uint32_t, uint16_t>::type;
+
+  static __device__ __forceinline__ u32x4_t load(const void* x, int64_t at, int c, int vocab) {
+    const E* p = static_cast<const E*>(x) + at + c;
+    if (c + VE <= vocab) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+    uint32_t e[VE];
+#pragma unroll
+    for (int k = 0; k < VE; ++k) e[k] = c + k < vocab ? (uint32_t)p[k] : 0u;
+    if constexpr (F32) return u32x4_t{e[0], e[1], e[2], e[3]};
+    else return u32x4_t{e[0] | e[1] << 16, e[2] | e[3] << 16, e[VE - 4] | e[VE - 3] << 16,
+                        e[VE - 2] | e[VE - 1] << 16};
+  }
+
+  static __device__ __forceinline__ void store(void* x, int64_t at, int c, int vocab, u32x4_t t) {
+    E* p = static_cast<E*>(x) + at + c;
+    if (c + VE <= vocab) {
+      __builtin_nontemporal_store(t, reinterpret_cast<V*>(p));
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < VE; ++k)
+      if (c + k < vocab) p[k] = (E)(F32 ? t[k] : t[k / 2] >> (16 * (k % 2)));
+  }
+
+  static __device__ __forceinline__ float get(u32x4_t t, int k) {
+    if constexpr (F32) return __uint_as_float(t[k]);
+    else return k % 2 == 0 ? bf_lo(t[k / 2]) : bf_hi(t[k / 2]);
+  }
+
+  static __device__ __forceinline__ u32x4_t put(const float (&d)[VE]) {
+    if constexpr (F32)
+      return u32x4_t{__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]),
+                     __float_as_uint(d[3])};
+    else
+      return u32x4_t{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[VE - 4], d[VE - 3]),
+                     pack_bf16(d[VE - 2], d[VE - 1])};
+  }
+};
+
+template <bool F32, bool SCALED>
+__global__ void __launch_bounds__(256)
+logprob_grad_kernel(const LogprobGradArgs a, int strips, int tile_rows, float* parts) {
+  using L = LpVec<F32>;
+  constexpr int VE = L::VE, AHEAD = 4;
+  __shared__ LpRowGrad rg[kLpTileRows];
+  const int64_t tile = blockIdx.x / strips;
+  const int c0 = (int)(blockIdx.x % strips) * 256 * VE;
+  const int c = c0 + threadIdx.x * VE;
+  const int64_t row0 = tile * tile_rows;
+  const int rows = (int)(a.rows - row0 < tile_rows ? a.rows - row0 : tile_rows);
+  if ((int)threadIdx.x < rows) rg[threadIdx.x] = lp_row_grad(a, row0 + threadIdx.x);
+  float sc[VE], sum[VE] = {};
+#pragma unroll
+  for (int k = 0; k < VE; ++k) sc[k] = SCALED && c + k < a.vocab ? a.scale[c + k] : 1.f;
+  __syncthreads();
+  if (c >= a.vocab) return;
+  for (int r0 = 0; r0 < rows; r0 += AHEAD) {
+    u32x4_t t[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (r0 + i < rows) t[i] = L::load(a.x, (row0 + r0 + i) * a.ld, c, a.vocab);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (r0 + i >= rows) break;
+      const LpRowGrad r = rg[r0 + i];
+      float d[VE];
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        float z = L::get(t[i], k);
+        if constexpr (SCALED) z = z * sc[k];
+        if (a.inv_temp != 1.f) z = z * a.inv_temp;
+        const float lp = fmaxf(z - r.lse, -200.f);
+        d[k] = lp_exp(lp) * __builtin_fmaf(r.gh, lp, r.c);
+      }
+      if (r.label >= c0 && r.label < c0 + 256 * VE) {               // uniform
+#pragma unroll
+        for (int k = 0; k < VE; ++k)
+          if (c + k == r.label && L::get(t[i], k) > -__builtin_inff()) d[k] += r.hot;
+      }
+      if constexpr (SCALED) {
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+          if (parts != nullptr)
+            sum[k] = __builtin_fmaf(d[k], fmaxf(L::get(t[i], k), -0x1.fffffep127f), sum[k]);
+          d[k] = d[k] * sc[k];
+        }
+      }
+      L::store(a.dx, (row0 + r0 + i) * a.ldo, c, a.vocab, L::put(d));
+    }
+  }
+  if constexpr (SCALED) {
+    if (parts != nullptr) {
+#pragma unroll
+      for (int k = 0; k < VE; ++k)
+        if (c + k < a.vocab) parts[tile * a.vocab + c + k] = sum[k];
+    }
   }
 }
 
-// The scale's gradient: one thread per column, down the rows.
-template <bool F32>
-__global__ void __launch_bounds__(64) logprob_scale_grad_kernel(const LogprobGradArgs a) {
-  const int col = blockIdx.x * 64 + threadIdx.x;
-  if (col >= a.vocab) return;
+// Adds the tiles' column sums, in order.
+__global__ void __launch_bounds__(64)
+logprob_scale_sum_kernel(const float* parts, int64_t tiles, int vocab, float* dscale) {
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (c >= vocab) return;
   float t = 0.f;
-  for (int64_t row = 0; row < a.rows; ++row) {
-    const LpRowGrad r = lp_row_grad(a, row);
-    const float x = lp_load<F32>(a.x, row * a.ld + col);
-    const float d = lp_dz(r, lp_z(x, a.scale, col, a.inv_temp), col, a.inv_temp);
-    t += d != 0.f ? d * x : 0.f;
-  }
-  a.dscale[col] = t;
+#pragma unroll 8
+  for (int64_t i = 0; i < tiles; ++i) t += parts[i * vocab + c];
+  dscale[c] = t;
 }
 
-hipError_t launch_logprob_rows_backward(bool f32, const LogprobGradArgs& a, void* workspace,
-                                        hipStream_t stream) {
-  (void)workspace;
-  // dscale first: dlogits may overwrite the logits
-  if (a.dscale != nullptr) {
-    const int grid = (a.vocab + 63) / 64;
-    if (f32) logprob_scale_grad_kernel<true><<<grid, 64, 0, stream>>>(a);
-    else logprob_scale_grad_kernel<false><<<grid, 64, 0, stream>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  constexpr int64_t kMostRows = 1 << 20;
-  for (int64_t r0 = 0; r0 < a.rows; r0 += kMostRows) {
+static int lp_strips(bool f32, int64_t vocab) {
+  const int64_t w = f32 ? 1024 : 2048;
+  return (int)((vocab + w - 1) / w);
+}
+
+// Rows of a tile: 8 to 128, about 2,048 workgroups in all.  A rule of the
+// sizes alone (the type's strip width aside: the narrower is taken for both),
+// so the order of dscale's sums is too.
+static int lp_tile_rows(int64_t rows, int64_t vocab) {
+  const int64_t want = rows * lp_strips(false, vocab) / 2048;
+  int t = 8;
+  while (t < kLpTileRows && t < want) t *= 2;
+  return t;
+}
+
+int64_t logprob_grad_workspace(int64_t rows, int64_t vocab) {
+  const int t = lp_tile_rows(rows, vocab);
+  return (rows + t - 1) / t * vocab * 4;
+}
+
+template <bool F32, bool SCALED>
+static hipError_t run_logprob_grad(const LogprobGradArgs& a, float* parts, hipStream_t stream) {
+  const int strips = lp_strips(F32, a.vocab), t = lp_tile_rows(a.rows, a.vocab);
+  const int64_t tiles = (a.rows + t - 1) / t;
+  // launches of at most 2^20 tiles' strips (a grid's limit is 2^31 threads)
+  const int64_t most = std::max<int64_t>(1, (1 << 20) / strips);
+  for (int64_t t0 = 0; t0 < tiles; t0 += most) {
+    const int64_t n = std::min(most, tiles - t0), r0 = t0 * t;
     LogprobGradArgs p = a;
-    const int64_t n = a.rows - r0 < kMostRows ? a.rows - r0 : kMostRows;
-    p.x = static_cast<const char*>(a.x) + r0 * a.ld * (f32 ? 4 : 2);
-    p.dx = static_cast<char*>(a.dx) + r0 * a.ldo * (f32 ? 4 : 2);
+    p.rows = std::min(n * t, a.rows - r0);
+    p.x = static_cast<const char*>(a.x) + r0 * a.ld * (F32 ? 4 : 2);
+    p.dx = static_cast<char*>(a.dx) + r0 * a.ldo * (F32 ? 4 : 2);
     if (a.labels != nullptr) p.labels = static_cast<const char*>(a.labels) + r0 * a.label_bytes;
     p.lse = a.lse + r0;
     if (a.entropy != nullptr) p.entropy = a.entropy + r0;
     if (a.dlogp != nullptr) p.dlogp = a.dlogp + r0;
     if (a.dentropy != nullptr) p.dentropy = a.dentropy + r0;
-    if (f32) logprob_grad_kernel<true><<<(int)n, kLpThreads, 0, stream>>>(p);
-    else logprob_grad_kernel<false><<<(int)n, kLpThreads, 0, stream>>>(p);
+    logprob_grad_kernel<F32, SCALED><<<(int)(n * strips), 256, 0, stream>>>(
+        p, strips, t, parts != nullptr ? parts + t0 * a.vocab : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return hipSuccess;
+  if (a.dscale == nullptr) return hipSuccess;        // (no rows: no parts, and zeros)
+  logprob_scale_sum_kernel<<<(a.vocab + 63) / 64, 64, 0, stream>>>(parts, tiles, a.vocab, a.dscale);
+  return hipGetLastError();
+}
+
+hipError_t launch_logprob_rows_backward(bool f32, const LogprobGradArgs& a, void* workspace,
+                                        hipStream_t stream) {
+  float* parts = a.dscale != nullptr ? static_cast<float*>(workspace) : nullptr;
+  if (f32)
+    return a.scale != nullptr ? run_logprob_grad<true, true>(a, parts, stream)
+                              : run_logprob_grad<true, false>(a, parts, stream);
+  return a.scale != nullptr ? run_logprob_grad<false, true>(a, parts, stream)
+                            : run_logprob_grad<false, false>(a, parts, stream);
 }
 
 }  // namespace dsr

@@ -69,6 +69,7 @@ struct LogprobArgs {
   int32_t label_bytes;
   float inv_temp;
 };
+int64_t logprob_workspace(int64_t rows, int64_t vocab, int top_k);
 hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace, hipStream_t stream);
 
 struct LogprobGradArgs {
@@ -87,6 +88,7 @@ struct LogprobGradArgs {
   int32_t label_bytes;
   float inv_temp;
 };
+int64_t logprob_grad_workspace(int64_t rows, int64_t vocab);
 hipError_t launch_logprob_rows_backward(bool f32, const LogprobGradArgs& a, void* workspace,
                                         hipStream_t stream);
 

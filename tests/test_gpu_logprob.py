@@ -220,6 +220,22 @@ def test_row_bits_do_not_depend_on_the_batch(B):
             assert torch.equal(bits(a[400:400 + rows]), bits(b))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_thousands_of_rows(B, kind):
+    """From 4,096 rows on a workgroup takes four of them: bits as for fewer."""
+    import torch
+    c = Case(4099, 2500, kind, 17)
+    x, labels, scale = c.logits(), dev(c.labels), dev(c.scale)
+    announce("logprob of 4,099 rows", kind)
+    whole = B.ds_logprob_rows(x, labels, scale, 1.0, 9)
+    for r0, rows in ((0, 5), (1021, 1400), (4094, 5)):
+        part = B.ds_logprob_rows(x[r0:r0 + rows], labels[r0:r0 + rows], scale, 1.0, 9)
+        torch.cuda.synchronize()
+        for a, b in zip(whole, part):
+            assert torch.equal(bits(a[r0:r0 + rows]), bits(b))
+    check(c, whole, 9)
+
+
 def test_outputs_one_at_a_time(B):
     import torch
     c = Case(4, 10007, "bf16", 10)
