@@ -73,8 +73,8 @@ int ds_embed_rows(const void* table, int32_t table_type, int64_t vocab, const vo
  *   dtable[t] = scale * sum_{i : ids_i = t} dy_i              (accumulate 0)
  *   dtable[t] = dtable[t] + scale * sum_{i : ids_i = t} dy_i  (accumulate 1)
  *
- * The rows of one token are summed in fp32 in ascending i: runs of 32 rows
- * first, then the runs.  With accumulate 0 every row of dtable is written
+ * The rows of one token are summed in fp32 in ascending i, long stretches of
+ * them by runs of 32 rows first.  With accumulate 0 every row of dtable is written
  * (zeros for a token that does not occur); with 1 only the rows of tokens
  * that occur are touched, so a tied head's gradient may already be there.
  *

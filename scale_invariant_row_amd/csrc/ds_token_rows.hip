@@ -79,7 +79,7 @@ int64_t ds_embed_rows_backward_workspace(int64_t vocab, int64_t rows, int64_t co
   int st = check_embed(DS_TYPE_F32, vocab, 8, 1.f, rows, cols);
   if (st != DS_OK) return st;
   if (rows > INT32_MAX) return DS_ERR_SHAPE;
-  return 0;
+  return vocab == 0 ? 0 : dsr::embed_grad_workspace(vocab, rows, cols);
 }
 
 int ds_embed_rows_backward(const uint16_t* dy, const void* ids, int32_t id_bytes, float scale,

@@ -28,6 +28,7 @@ struct EmbedGradArgs {
   int32_t accumulate;
   float scale;
 };
+int64_t embed_grad_workspace(int64_t vocab, int64_t rows, int64_t cols);
 hipError_t launch_embed_rows_backward(bool f32, bool wide_ids, const EmbedGradArgs& a,
                                       void* workspace, hipStream_t stream);
 
