@@ -18,6 +18,7 @@ namespace {
 using namespace dsh;
 
 constexpr int64_t kMostBytes = INT64_MAX / 8;
+constexpr int64_t kMostGradRows = 1 << 30;   // of an embedding's gradient
 
 bool type_ok(int32_t t) { return t == DS_TYPE_BF16 || t == DS_TYPE_F32; }
 int64_t type_bytes(int32_t t) { return t == DS_TYPE_F32 ? 4 : 2; }
@@ -78,7 +79,7 @@ int ds_embed_rows(const void* table, int32_t table_type, int64_t vocab, const vo
 int64_t ds_embed_rows_backward_workspace(int64_t vocab, int64_t rows, int64_t cols) {
   int st = check_embed(DS_TYPE_F32, vocab, 8, 1.f, rows, cols);
   if (st != DS_OK) return st;
-  if (rows > INT32_MAX) return DS_ERR_SHAPE;
+  if (rows > kMostGradRows) return DS_ERR_SHAPE;
   return vocab == 0 ? 0 : dsr::embed_grad_workspace(vocab, rows, cols);
 }
 
@@ -88,7 +89,7 @@ int ds_embed_rows_backward(const uint16_t* dy, const void* ids, int32_t id_bytes
                            ds_stream_t stream) {
   int st = check_embed(grad_type, vocab, id_bytes, scale, rows, cols);
   if (st != DS_OK) return st;
-  if (rows > INT32_MAX) return DS_ERR_SHAPE;
+  if (rows > kMostGradRows) return DS_ERR_SHAPE;
   if (accumulate != 0 && accumulate != 1) return DS_ERR_ARG;
   if (vocab == 0 || (rows == 0 && accumulate)) return DS_OK;
   if (dtable == nullptr || (rows > 0 && (dy == nullptr || ids == nullptr))) return DS_ERR_NULL;

@@ -2,6 +2,8 @@
 //
 //   out_i     = bf16(scale * table[ids_i])          (zeros for an id outside the table)
 //   dtable[t] = scale * sum_{i : ids_i = t} dy_i    fp32 sums in ascending i
+#include <type_traits>
+
 #include "row_kernels.hpp"
 #include "token_launch.hpp"
 
@@ -14,7 +16,7 @@ __device__ __forceinline__ int32_t token_at(const void* ids, int64_t i, int64_t 
   return t >= 0 && t < vocab ? (int32_t)t : -1;
 }
 
-// One wave per row; lane l holds 8 columns of each stretch of 512.
+// One wave per row and 16 bytes a lane and load: 4 fp32 or 8 bf16 columns.
 template <bool F32, class Id>
 __global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedArgs a) {
   const int lane = threadIdx.x & 63;
@@ -27,22 +29,26 @@ __global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedArgs a) {
   const RowBuf ib(F32 ? (const void*)(static_cast<const float*>(a.table) + at)
                       : (const void*)(static_cast<const uint16_t*>(a.table) + at), bytes);
   const RowBuf ob(a.out + row * a.cols, (uint32_t)a.cols * 2u);
-  for (int c = lane * 8; c < a.cols; c += 512) {
-    float v[8];
-    if constexpr (F32) {
-      const f32x4_t x = ib.ld16f_cached(c * 4), y = ib.ld16f_cached(c * 4 + 16);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    } else {
-      const u32x4_t x = __builtin_bit_cast(u32x4_t, ib.ld16f_cached(c * 2));
-      v[0] = bf_lo(x.x); v[1] = bf_hi(x.x); v[2] = bf_lo(x.y); v[3] = bf_hi(x.y);
-      v[4] = bf_lo(x.z); v[5] = bf_hi(x.z); v[6] = bf_lo(x.w); v[7] = bf_hi(x.w);
+  constexpr int STEP = F32 ? 256 : 512, N = 4;             // columns a load of the wave, loads ahead
+  for (int c0 = 0; c0 < a.cols; c0 += STEP * N) {
+    f32x4_t x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = ib.ld16f_cached((c0 + i * STEP) * (F32 ? 4 : 2) + lane * 16);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (F32) {
+        ob.st8(u32x2_t{pack_bf16(x[i].x * a.scale, x[i].y * a.scale),
+                       pack_bf16(x[i].z * a.scale, x[i].w * a.scale)},
+               (c0 + i * STEP) * 2 + lane * 8);
+      } else {
+        const u32x4_t b = __builtin_bit_cast(u32x4_t, x[i]);
+        ob.st16(u32x4_t{pack_bf16(bf_lo(b.x) * a.scale, bf_hi(b.x) * a.scale),
+                        pack_bf16(bf_lo(b.y) * a.scale, bf_hi(b.y) * a.scale),
+                        pack_bf16(bf_lo(b.z) * a.scale, bf_hi(b.z) * a.scale),
+                        pack_bf16(bf_lo(b.w) * a.scale, bf_hi(b.w) * a.scale)},
+                (c0 + i * STEP) * 2 + lane * 16);
+      }
     }
-    const u32x4_t o = {pack_bf16(v[0] * a.scale, v[1] * a.scale),
-                       pack_bf16(v[2] * a.scale, v[3] * a.scale),
-                       pack_bf16(v[4] * a.scale, v[5] * a.scale),
-                       pack_bf16(v[6] * a.scale, v[7] * a.scale)};
-    ob.st16(o, c * 2);
   }
 }
 
@@ -57,12 +63,12 @@ hipError_t launch_embed_rows(bool f32, bool wide_ids, const EmbedArgs& a, int gr
 
 // ---------------------------------------------------------------- gradient
 //
-// Three steps: sort the rows by token (embed_sort_kernel), sum every whole
-// run of 32 sorted rows that share one token (embed_run_kernel), and write the
-// table (embed_table_kernel).  A token's rows are added in ascending order,
-// its whole runs by their sums, so the order is fixed by the ids and no token,
-// however often it occurs, makes one wave read more than 62 rows and a 32nd
-// of the rest.
+// Three steps: sort the rows by token, clearing the table meanwhile
+// (embed_sort_kernel), sum them by blocks of 32 sorted rows
+// (embed_sum_kernel), and join the sums of tokens that span blocks
+// (embed_join_kernel).  A token's rows are added in ascending order within a
+// block and its blocks in order, so the ids fix the order of every sum, and no
+// token, however often it occurs, holds one wave up for all its rows.
 //
 // Tokens are dealt over `parts` groups, a power of two: token t is number
 // t / parts of group t mod parts, so that the frequent low ids of a frequency-
@@ -72,40 +78,60 @@ hipError_t launch_embed_rows(bool f32, bool wide_ids, const EmbedArgs& a, int gr
 constexpr int kSortThreads = 1024;
 constexpr int kSortRows = 4;                              // ids a lane holds of a block
 constexpr int kSortBlock = kSortThreads * kSortRows;      // 4,096 ids
-constexpr int kSortCap = kSortBlock;                      // rows sorted at once
+constexpr int kSortCap = kSortBlock;                      // rows kept in LDS
+constexpr int kClearVectors = 8 * kSortThreads;           // cleared by a workgroup: 128 KiB
 constexpr int kSortBins = 2048;                           // most tokens of a group
 constexpr int kRun = 32;
+constexpr int kAhead = 16;                                // of them loaded at a time
 
 // The workspace: start[parts * bins + 1] (first sorted row of each token),
-// order[rows] and token[rows] (row and token in sorted order), run sums
-// [rows / 32][cols].
+// order[rows] and token[rows] (row and token in sorted order), parts of sums
+// [blocks of 32 rows][2][cols].
 struct EmbedSort {
   int32_t log_parts, bins, bin_bits;
   int32_t* start;
   int32_t* order;
   int32_t* token;
-  float* run;
+  float* part;
 };
 
 // One workgroup per group.  It reads every id, 4,096 at a time, and keeps its
-// own in LDS in their order (a wave's ids are 256 in a row, so ballots and the
-// counts of the waves before give each its place), counting them by token and
-// counting the rows of the groups before.  Then a stable sort by token: a
-// split by each bit of the token's number.  Only a group of more than 4,096
-// rows reads the ids a second time, and sorts 4,096 at a time, each going
-// behind what its token already has.  Reading all ids in every workgroup
-// costs parts * rows * 8 bytes from L2 (67 MB for 32,768 ids), and one launch
-// takes the place of the dozen that a device-wide radix sort would need.
+// own rows in LDS in their order (a wave's ids are 256 in a row, so ballots and
+// the counts of the waves before give each its place), counting them by token
+// and counting the rows of the groups before.  The counts give each token its
+// first place; the rows then go to their places in order: ballots over the
+// bits of the token's number find a lane's equals among 64 rows, the first of
+// them moves the token's cursor for all, and the waves take turns.  Only a
+// group of more than 4,096 rows reads the ids a second time.  Reading all ids
+// in every workgroup costs parts * rows * 8 bytes from L2 (67 MB for 32,768
+// ids); one launch takes the place of the dozen of a device-wide radix sort.
+//
+// The workgroups past the groups clear the table meanwhile (`vectors` of 16
+// bytes; none when the gradient is added to what is there).  The rows of
+// tokens that occur are written again (160 MB of 2.1 GB for 32,768 Zipf-like
+// ids of 131,072), which costs less than looking up, row by row, which do
+// not: together with the sort and the sums 478 us, where a launch that wrote
+// zeros or sums token by token took 468 to 517 in its variants, but 32 instead
+// of 27 us for 1,021 ids of 50,304 x 768.  In a launch of its own the clearing
+// took 351 us and the sort 24 behind it.
 template <class Id>
-__global__ void __launch_bounds__(kSortThreads)
-embed_sort_kernel(const void* ids, int rows, int vocab, const EmbedSort w) {
+__global__ void __launch_bounds__(kSortThreads, 8)     // 64 VGPRs: two workgroups a compute unit
+embed_sort_kernel(const void* ids, int rows, int vocab, const EmbedSort w, u32x4_t* table,
+                  int64_t vectors) {
   __shared__ uint32_t cursor[kSortBins];
-  __shared__ uint32_t pos[2][kSortCap];
-  __shared__ uint16_t bin[2][kSortCap];
+  __shared__ uint32_t pos[kSortCap];
+  __shared__ uint16_t bin[kSortCap];
   __shared__ uint32_t wsum[2][16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int group = blockIdx.x, mask = (1 << w.log_parts) - 1;
+  if (group > mask) {
+    const int64_t v0 = (int64_t)(group - mask - 1) * kClearVectors + tid;
+#pragma unroll
+    for (int i = 0; i < kClearVectors / kSortThreads; ++i)
+      if (v0 + i * kSortThreads < vectors) table[v0 + i * kSortThreads] = u32x4_t{0u, 0u, 0u, 0u};
+    return;
+  }
   const uint64_t below = (1ull << lane) - 1;
   int flip = 0;
   // exclusive prefix over the waves of v (uniform in a wave), and the total;
@@ -127,63 +153,44 @@ embed_sort_kernel(const void* ids, int rows, int vocab, const EmbedSort w) {
   for (int i = tid; i < w.bins; i += kSortThreads) cursor[i] = 0;
   __syncthreads();
 
-  // Sorts the n rows in pos[0], bin[0] by token and writes them out behind
-  // their tokens' cursors.
+  // Writes the n rows kept in pos, bin to their places.
   auto flush = [&](uint32_t n) {
-    int f = 0;
     __syncthreads();
-    for (int b = 0; b < w.bin_bits; ++b) {
-      uint32_t p[kSortRows], q[kSortRows];
-      uint64_t zeros[kSortRows];
-      uint32_t nz = 0;
+    uint32_t p[kSortRows], q[kSortRows];
+    uint64_t same[kSortRows];
 #pragma unroll
-      for (int j = 0; j < kSortRows; ++j) {
-        const uint32_t e = wave * 64 * kSortRows + j * 64 + lane;
-        p[j] = e < n ? pos[f][e] : 0;
-        q[j] = e < n ? bin[f][e] : 0;
-        zeros[j] = __builtin_amdgcn_ballot_w64(e < n && ((q[j] >> b) & 1) == 0);
-        nz += __builtin_popcountll(zeros[j]);
+    for (int j = 0; j < kSortRows; ++j) {
+      const uint32_t e = wave * 64 * kSortRows + j * 64 + lane;
+      p[j] = e < n ? pos[e] : 0;
+      q[j] = e < n ? bin[e] : 0;
+      same[j] = __builtin_amdgcn_ballot_w64(e < n);
+      if (same[j] == 0) continue;
+      for (int b = 0; b < w.bin_bits; ++b) {
+        const uint64_t ones = __builtin_amdgcn_ballot_w64((q[j] >> b & 1) != 0);
+        same[j] &= (q[j] >> b & 1) != 0 ? ones : ~ones;
       }
-      uint32_t total;
-      uint32_t z = wave_prefix(nz, total);
+    }
+    const int turns = (int)((n + 64 * kSortRows - 1) / (64 * kSortRows));
+    for (int v = 0; v < turns; ++v) {
+      if (v == wave) {
+        uint32_t at[kSortRows];
 #pragma unroll
-      for (int j = 0; j < kSortRows; ++j) {
-        const uint32_t e = wave * 64 * kSortRows + j * 64 + lane;
-        const uint32_t mine = z + __builtin_popcountll(zeros[j] & below);   // zeros before e
-        const uint32_t to = ((q[j] >> b) & 1) == 0 ? mine : total + e - mine;
-        if (e < n) {
-          pos[f ^ 1][to] = p[j];
-          bin[f ^ 1][to] = (uint16_t)q[j];
+        for (int j = 0; j < kSortRows; ++j) {
+          const bool first = (same[j] & below) == 0 && (same[j] >> lane & 1) != 0;
+          at[j] = first ? atomicAdd(&cursor[q[j]], (uint32_t)__builtin_popcountll(same[j])) : 0;
         }
-        z += __builtin_popcountll(zeros[j]);
+#pragma unroll
+        for (int j = 0; j < kSortRows; ++j) {
+          const uint32_t base = __shfl(at[j], same[j] != 0 ? __builtin_ctzll(same[j]) : 0);
+          if ((same[j] >> lane & 1) != 0) {
+            const uint32_t to = base + __builtin_popcountll(same[j] & below);
+            w.order[to] = (int32_t)p[j];
+            w.token[to] = (int32_t)((q[j] << w.log_parts) | (uint32_t)group);
+          }
+        }
       }
-      f ^= 1;
       __syncthreads();
     }
-    uint32_t first[kSortRows];
-#pragma unroll
-    for (int j = 0; j < kSortRows; ++j) {
-      const uint32_t e = tid + j * kSortThreads;
-      if (e >= n) continue;
-      const uint32_t q = bin[f][e];
-      uint32_t lo = 0, hi = e;                            // first entry of e's token
-      while (lo < hi) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (bin[f][mid] < q) lo = mid + 1;
-        else hi = mid;
-      }
-      first[j] = lo;
-      const uint32_t to = cursor[q] + (e - lo);
-      w.order[to] = (int32_t)pos[f][e];
-      w.token[to] = (int32_t)((q << w.log_parts) | (uint32_t)group);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kSortRows; ++j) {
-      const uint32_t e = tid + j * kSortThreads;
-      if (e < n && (e + 1 == n || bin[f][e + 1] != bin[f][e])) cursor[bin[f][e]] += e + 1 - first[j];
-    }
-    __syncthreads();
   };
 
   // first reading: count, and keep the first 4,096
@@ -196,25 +203,27 @@ embed_sort_kernel(const void* ids, int rows, int vocab, const EmbedSort w) {
       to[j] = i < rows ? token_at<Id>(ids, i, vocab) : -1;
     }
   };
-  // the block's rows of this group into pos[0], bin[0] from `at` on
+  // the block's rows of this group into pos, bin from `at` on
+  uint64_t hits[kSortRows];
   auto place = [&](int base, uint32_t at) {
 #pragma unroll
     for (int j = 0; j < kSortRows; ++j) {
-      const bool mine = t[j] >= 0 && (t[j] & mask) == group;
-      const uint64_t hits = __builtin_amdgcn_ballot_w64(mine);
-      const uint32_t to = at + __builtin_popcountll(hits & below);
-      if (mine && to < kSortCap) {
-        pos[0][to] = (uint32_t)(base + wave * 64 * kSortRows + j * 64 + lane);
-        bin[0][to] = (uint16_t)(t[j] >> w.log_parts);
+      if (hits[j] == 0) continue;
+      const uint32_t to = at + __builtin_popcountll(hits[j] & below);
+      if ((hits[j] >> lane & 1) != 0 && to < kSortCap) {
+        pos[to] = (uint32_t)(base + wave * 64 * kSortRows + j * 64 + lane);
+        bin[to] = (uint16_t)(t[j] >> w.log_parts);
       }
-      at += __builtin_popcountll(hits);
+      at += __builtin_popcountll(hits[j]);
     }
   };
   auto count = [&]() {
     uint32_t n = 0;
 #pragma unroll
-    for (int j = 0; j < kSortRows; ++j)
-      n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(t[j] >= 0 && (t[j] & mask) == group));
+    for (int j = 0; j < kSortRows; ++j) {
+      hits[j] = __builtin_amdgcn_ballot_w64(t[j] >= 0 && (t[j] & mask) == group);
+      n += __builtin_popcountll(hits[j]);
+    }
     return n;
   };
   read(0, next);
@@ -229,6 +238,7 @@ embed_sort_kernel(const void* ids, int rows, int vocab, const EmbedSort w) {
     }
     uint32_t total;
     const uint32_t before = wave_prefix(count(), total);
+    if (total == 0) continue;
     place((int)base, kept + before);
     kept += total;
   }
@@ -275,125 +285,169 @@ embed_sort_kernel(const void* ids, int rows, int vocab, const EmbedSort w) {
   flush(kept);
 }
 
-// v[VN][8] += the bf16 row at `row`, columns c + 512 k of the lane.
-template <int VN>
-__device__ __forceinline__ void load_row(u32x4_t (&x)[VN], const uint16_t* dy, int64_t row,
-                                         int cols, int c) {
-  const RowBuf b(dy + row * cols, (uint32_t)cols * 2u);
-#pragma unroll
-  for (int k = 0; k < VN; ++k) x[k] = b.ld16((c + 512 * k) * 2);
-}
+// A wave's columns: VE a lane, 4 where the table is fp32 and 8 where it is
+// bf16, so that its stores cover 1 KiB without gaps (with 8 columns a lane,
+// non-temporal fp32 stores of alternate 16 bytes reached 2.3 TB/s).
+template <bool F32>
+struct EmbedCols {
+  static constexpr int VE = F32 ? 4 : 8;
+  using Raw = typename std::conditional<F32, u32x2_t, u32x4_t>::type;   // of a row of dy
+  using Old = u32x4_t;                                                  // of a row of the table
+  float v[VE];
 
-template <int VN>
-__device__ __forceinline__ void add_row(float (&acc)[VN][8], const u32x4_t (&x)[VN]) {
-#pragma unroll
-  for (int k = 0; k < VN; ++k) {
-    acc[k][0] += bf_lo(x[k].x); acc[k][1] += bf_hi(x[k].x);
-    acc[k][2] += bf_lo(x[k].y); acc[k][3] += bf_hi(x[k].y);
-    acc[k][4] += bf_lo(x[k].z); acc[k][5] += bf_hi(x[k].z);
-    acc[k][6] += bf_lo(x[k].w); acc[k][7] += bf_hi(x[k].w);
+  static __device__ __forceinline__ Raw load(const EmbedGradArgs& a, int row, int c) {
+    const RowBuf b(a.dy + (int64_t)row * a.cols, (uint32_t)a.cols * 2u);
+    if constexpr (F32) return b.ld8(c * 2);
+    else return b.ld16(c * 2);
   }
-}
 
-// acc += the rows order[from .. to), in order, four loads ahead.
-template <int VN>
-__device__ __forceinline__ void add_rows(float (&acc)[VN][8], const uint16_t* dy,
-                                         const int32_t* order, int from, int to, int cols, int c,
-                                         int lane) {
-  for (int p0 = from; p0 < to; p0 += 64) {
-    const int n = min(64, to - p0);
-    const int mine = lane < n ? order[p0 + lane] : 0;
-    for (int i = 0; i < n; i += 4) {
-      u32x4_t x[4][VN];
+  __device__ __forceinline__ void add(Raw x) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u < n) load_row<VN>(x[u], dy, __builtin_amdgcn_readlane(mine, i + u), cols, c);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u < n) add_row<VN>(acc, x[u]);
+    for (int j = 0; j < VE / 2; ++j) {
+      v[2 * j] += bf_lo(x[j]);
+      v[2 * j + 1] += bf_hi(x[j]);
     }
   }
-}
 
-// Sums of the whole runs of 32 sorted rows that share a token, one wave per
-// run and 512 VN columns.
-template <int VN>
-__global__ void __launch_bounds__(256) embed_run_kernel(const EmbedGradArgs a, const EmbedSort w) {
-  const int lane = threadIdx.x & 63;
-  const int k = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int known = w.start[(int64_t)w.bins << w.log_parts];
-  if ((int64_t)(k + 1) * kRun > known || w.token[k * kRun] != w.token[k * kRun + kRun - 1]) return;
-  const int c = blockIdx.y * 512 * VN + lane * 8;
-  float acc[VN][8] = {};
-  add_rows<VN>(acc, a.dy, w.order, k * kRun, (k + 1) * kRun, a.cols, c, lane);
-  const RowBuf b(w.run + (int64_t)k * a.cols, (uint32_t)a.cols * 4u);
-#pragma unroll
-  for (int v = 0; v < VN; ++v) {
-    b.st16(__builtin_bit_cast(u32x4_t, f32x4_t{acc[v][0], acc[v][1], acc[v][2], acc[v][3]}),
-           (c + 512 * v) * 4);
-    b.st16(__builtin_bit_cast(u32x4_t, f32x4_t{acc[v][4], acc[v][5], acc[v][6], acc[v][7]}),
-           (c + 512 * v) * 4 + 16);
+  // sums of a part of a token's rows, in the workspace
+  static __device__ __forceinline__ RowBuf part(const EmbedGradArgs& a, const EmbedSort& w, int k,
+                                                int which) {
+    return RowBuf(w.part + ((int64_t)k * 2 + which) * a.cols, (uint32_t)a.cols * 4u);
   }
-}
+  __device__ __forceinline__ void store_part(const RowBuf& b, int c) const {
+#pragma unroll
+    for (int h = 0; h < VE; h += 4)
+      b.st16(__builtin_bit_cast(u32x4_t, f32x4_t{v[h], v[h + 1], v[h + 2], v[h + 3]}), (c + h) * 4);
+  }
+  __device__ __forceinline__ void add_part(const RowBuf& b, int c) {
+#pragma unroll
+    for (int h = 0; h < VE; h += 4) {
+      const f32x4_t x = b.ld16f((c + h) * 4);
+      v[h] += x.x; v[h + 1] += x.y; v[h + 2] += x.z; v[h + 3] += x.w;
+    }
+  }
 
-// The table, one wave per token: zeros, or its rows' sum.
-template <bool F32, int VN>
-__global__ void __launch_bounds__(256) embed_table_kernel(const EmbedGradArgs a, const EmbedSort w) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (t >= a.vocab) return;
-  const int64_t slot = (t & ((1 << w.log_parts) - 1)) * w.bins + (t >> w.log_parts);
-  const int s = __builtin_amdgcn_readfirstlane(w.start[slot]);
-  const int e = __builtin_amdgcn_readfirstlane(w.start[slot + 1]);
-  if (s == e && a.accumulate) return;
-  const RowBuf ob(F32 ? (const void*)(static_cast<float*>(a.dtable) + t * a.cols)
-                      : (const void*)(static_cast<uint16_t*>(a.dtable) + t * a.cols),
+  static __device__ __forceinline__ RowBuf table(const EmbedGradArgs& a, int t) {
+    return RowBuf(F32 ? (const void*)(static_cast<float*>(a.dtable) + (int64_t)t * a.cols)
+                      : (const void*)(static_cast<uint16_t*>(a.dtable) + (int64_t)t * a.cols),
                   (uint32_t)a.cols * (F32 ? 4u : 2u));
-  // every lane takes every turn (add_rows passes row numbers between lanes);
-  // columns past the row load 0 and store nothing
-  for (int c = lane * 8; c - lane * 8 < a.cols; c += 512 * VN) {
-    float acc[VN][8] = {};
-    const int k0 = (s + kRun - 1) / kRun, k1 = e / kRun;
-    if (k0 < k1) {
-      add_rows<VN>(acc, a.dy, w.order, s, k0 * kRun, a.cols, c, lane);
-      for (int k = k0; k < k1; ++k) {
-        const RowBuf b(w.run + (int64_t)k * a.cols, (uint32_t)a.cols * 4u);
+  }
+  static __device__ __forceinline__ Old load_old(const EmbedGradArgs& a, int t, int c) {
+    return table(a, t).ld16(c * (F32 ? 4 : 2));
+  }
+  // scale times the sum, plus what was there (if accumulating), to token t
+  __device__ __forceinline__ void store(const EmbedGradArgs& a, int t, int c, Old old) const {
+    float d[VE];
 #pragma unroll
-        for (int v = 0; v < VN; ++v) {
-          const f32x4_t x = b.ld16f((c + 512 * v) * 4), y = b.ld16f((c + 512 * v) * 4 + 16);
-          acc[v][0] += x.x; acc[v][1] += x.y; acc[v][2] += x.z; acc[v][3] += x.w;
-          acc[v][4] += y.x; acc[v][5] += y.y; acc[v][6] += y.z; acc[v][7] += y.w;
+    for (int j = 0; j < VE; ++j) d[j] = v[j] * a.scale;
+    if constexpr (F32) {
+      if (a.accumulate) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] += __uint_as_float(old[j]);
+      }
+      table(a, t).st16(__builtin_bit_cast(u32x4_t, f32x4_t{d[0], d[1], d[2], d[3]}), c * 4);
+    } else {
+      if (a.accumulate) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          d[2 * j] += bf_lo(old[j]);
+          d[VE - 7 + 2 * j] += bf_hi(old[j]);
         }
       }
-      add_rows<VN>(acc, a.dy, w.order, k1 * kRun, e, a.cols, c, lane);
-    } else if (s < e) {
-      add_rows<VN>(acc, a.dy, w.order, s, e, a.cols, c, lane);
-    }
-#pragma unroll
-    for (int v = 0; v < VN; ++v) {
-      const int at = c + 512 * v;
-      float d[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = acc[v][j] * a.scale;
-      if constexpr (F32) {
-        if (a.accumulate) {
-          const f32x4_t x = ob.ld16f(at * 4), y = ob.ld16f(at * 4 + 16);
-          d[0] += x.x; d[1] += x.y; d[2] += x.z; d[3] += x.w;
-          d[4] += y.x; d[5] += y.y; d[6] += y.z; d[7] += y.w;
-        }
-        ob.st16(__builtin_bit_cast(u32x4_t, f32x4_t{d[0], d[1], d[2], d[3]}), at * 4);
-        ob.st16(__builtin_bit_cast(u32x4_t, f32x4_t{d[4], d[5], d[6], d[7]}), at * 4 + 16);
-      } else {
-        if (a.accumulate) {
-          const u32x4_t x = ob.ld16(at * 2);
-          d[0] += bf_lo(x.x); d[1] += bf_hi(x.x); d[2] += bf_lo(x.y); d[3] += bf_hi(x.y);
-          d[4] += bf_lo(x.z); d[5] += bf_hi(x.z); d[6] += bf_lo(x.w); d[7] += bf_hi(x.w);
-        }
-        ob.st16(u32x4_t{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]),
-                        pack_bf16(d[6], d[7])}, at * 2);
-      }
+      table(a, t).st16(u32x4_t{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]),
+                               pack_bf16(d[VE - 4], d[VE - 3]), pack_bf16(d[VE - 2], d[VE - 1])},
+                       c * 2);
     }
   }
+};
+
+// Sums by blocks of 32 sorted rows: one wave per block and 64 VE columns, 16
+// loads in flight together.  The rows of a token that lies in the block
+// give its row of the table; of one that came from the block before, part 0
+// of the block; of one that only goes on into the next, part 1.
+//
+// Bound by memory: for 32,768 x 4,096 (0.43 GB read and written) 96 us.  Eight
+// loads at a time measured the same (98 us).  Waves that gathered all rows of
+// one token, four at a time, needed their whole runs of 32 summed by a launch
+// before (28 us) and took 83 us more, held up by the frequent tokens.
+template <bool F32>
+__global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedGradArgs a, const EmbedSort w, int tiles) {
+  using C = EmbedCols<F32>;
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t block = wave / tiles;
+  if (block * kRun >= a.rows) return;
+  const int k = (int)block, p0 = k * kRun;
+  const int c = (int)(wave % tiles) * (64 * C::VE) + lane * C::VE;   // past the row: loads 0, stores nothing
+  // all loads at once: what lies past the known rows is not used
+  const int known = __builtin_amdgcn_readfirstlane(w.start[(int64_t)w.bins << w.log_parts]);
+  const bool in = p0 + lane < a.rows && lane <= kRun;    // the block and one more
+  const int tok = in ? w.token[p0 + lane] : -1;
+  const int row = in ? w.order[p0 + lane] : 0;
+  const int left = k > 0 ? __builtin_amdgcn_readfirstlane(w.token[p0 - 1]) : -1;
+  const int n = min(kRun, known - p0);
+  if (n <= 0) return;
+  const int next = __shfl_down(tok, 1);
+  uint32_t ends = (uint32_t)__builtin_amdgcn_ballot_w64(lane < n && (lane == n - 1 || next != tok));
+  const bool from_left = left == __builtin_amdgcn_readlane(tok, 0);
+  const bool to_right = n == kRun && p0 + kRun < known &&
+                        __builtin_amdgcn_readlane(tok, kRun) == __builtin_amdgcn_readlane(tok, kRun - 1);
+  C acc{};
+  bool first = true;
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += kAhead) {
+    typename C::Raw x[kAhead];
+    typename C::Old old[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (j0 + j < n) x[j] = C::load(a, __builtin_amdgcn_readlane(row, j0 + j), c);
+    if (a.accumulate) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (ends >> (j0 + j) & 1) old[j] = C::load_old(a, __builtin_amdgcn_readlane(tok, j0 + j), c);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j0 + j >= n) break;
+      acc.add(x[j]);
+      if (!(ends >> (j0 + j) & 1)) continue;
+      const bool l = first && from_left, r = j0 + j == n - 1 && to_right;
+      if (l || r) acc.store_part(C::part(a, w, k, l ? 0 : 1), c);
+      else acc.store(a, __builtin_amdgcn_readlane(tok, j0 + j), c, old[j]);
+      acc = C{};
+      first = false;
+    }
+  }
+}
+
+// Tokens that span blocks: the wave of the block that a token starts in adds
+// part 1 of it and part 0 of the blocks that follow, in order.
+template <bool F32>
+__global__ void __launch_bounds__(256)
+embed_join_kernel(const EmbedGradArgs a, const EmbedSort w, int tiles) {
+  using C = EmbedCols<F32>;
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t block = wave / tiles;
+  if ((block + 1) * kRun >= a.rows) return;
+  const int k = (int)block, p0 = k * kRun;
+  const int known = __builtin_amdgcn_readfirstlane(w.start[(int64_t)w.bins << w.log_parts]);
+  // lane 0: the token left of the block; 1 and 2: its first and last; 3: the next
+  const int p = lane == 0 ? p0 - 1 : lane == 1 ? p0 : lane == 2 ? p0 + kRun - 1 : p0 + kRun;
+  const int tok = p >= 0 ? w.token[p] : -1;
+  const int t = __builtin_amdgcn_readlane(tok, 2);
+  if (p0 + kRun >= known || __builtin_amdgcn_readlane(tok, 3) != t) return;     // it ends here
+  if (__builtin_amdgcn_readlane(tok, 0) == t && __builtin_amdgcn_readlane(tok, 1) == t) return;   // began before
+  const int64_t slot = (int64_t)(t & ((1 << w.log_parts) - 1)) * w.bins + (t >> w.log_parts);
+  const int last = (__builtin_amdgcn_readfirstlane(w.start[slot + 1]) - 1) / kRun;
+  const int c = (int)(wave % tiles) * (64 * C::VE) + lane * C::VE;
+  C acc{};
+  acc.add_part(C::part(a, w, k, 1), c);
+  typename C::Old old{};
+  if (a.accumulate) old = C::load_old(a, t, c);
+#pragma unroll 8
+  for (int b = k + 1; b <= last; ++b) acc.add_part(C::part(a, w, b, 0), c);
+  acc.store(a, t, c, old);
 }
 
 static EmbedSort embed_sort_plan(int64_t vocab, int64_t rows, int64_t cols, void* workspace,
@@ -411,8 +465,8 @@ static EmbedSort embed_sort_plan(int64_t vocab, int64_t rows, int64_t cols, void
   w.start = reinterpret_cast<int32_t*>(p);
   w.order = reinterpret_cast<int32_t*>(p + ns);
   w.token = reinterpret_cast<int32_t*>(p + ns + nr);
-  w.run = reinterpret_cast<float*>(p + ns + 2 * nr);
-  *bytes = ns + 2 * nr + rows / kRun * cols * 4;
+  w.part = reinterpret_cast<float*>(p + ns + 2 * nr);
+  *bytes = ns + 2 * nr + (rows + kRun - 1) / kRun * 2 * cols * 4;
   return w;
 }
 
@@ -422,15 +476,15 @@ int64_t embed_grad_workspace(int64_t vocab, int64_t rows, int64_t cols) {
   return bytes;
 }
 
-template <bool F32, int VN>
+template <bool F32>
 static hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedSort& w, hipStream_t stream) {
-  if (a.rows >= kRun) {
-    const dim3 grid((unsigned)((a.rows / kRun + 3) / 4), (unsigned)((a.cols + 512 * VN - 1) / (512 * VN)));
-    embed_run_kernel<VN><<<grid, 256, 0, stream>>>(a, w);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  embed_table_kernel<F32, VN><<<(int)(((int64_t)a.vocab + 3) / 4), 256, 0, stream>>>(a, w);
+  constexpr int W = 64 * EmbedCols<F32>::VE;
+  const int tiles = (a.cols + W - 1) / W;
+  const int64_t waves = ((int64_t)a.rows + kRun - 1) / kRun * tiles;
+  embed_sum_kernel<F32><<<(int)((waves + 3) / 4), 256, 0, stream>>>(a, w, tiles);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.rows <= kRun) return e;
+  embed_join_kernel<F32><<<(int)((waves + 3) / 4), 256, 0, stream>>>(a, w, tiles);
   return hipGetLastError();
 }
 
@@ -438,17 +492,16 @@ hipError_t launch_embed_rows_backward(bool f32, bool wide_ids, const EmbedGradAr
                                       void* workspace, hipStream_t stream) {
   int64_t bytes = 0;
   const EmbedSort w = embed_sort_plan(a.vocab, a.rows, a.cols, workspace, &bytes);
-  const int groups = 1 << w.log_parts;
+  const int64_t vectors = a.accumulate ? 0 : (int64_t)a.vocab * a.cols / (f32 ? 4 : 8);
+  const int grid = (1 << w.log_parts) + (int)((vectors + kClearVectors - 1) / kClearVectors);
+  auto* table = static_cast<u32x4_t*>(a.dtable);
   if (wide_ids)
-    embed_sort_kernel<int64_t><<<groups, kSortThreads, 0, stream>>>(a.ids, a.rows, a.vocab, w);
+    embed_sort_kernel<int64_t><<<grid, kSortThreads, 0, stream>>>(a.ids, a.rows, a.vocab, w, table, vectors);
   else
-    embed_sort_kernel<int32_t><<<groups, kSortThreads, 0, stream>>>(a.ids, a.rows, a.vocab, w);
+    embed_sort_kernel<int32_t><<<grid, kSortThreads, 0, stream>>>(a.ids, a.rows, a.vocab, w, table, vectors);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  // a wave's columns: 512, 1,024 or 2,048 at a time
-  if (a.cols <= 512) return f32 ? run_embed_grad<true, 1>(a, w, stream) : run_embed_grad<false, 1>(a, w, stream);
-  if (a.cols <= 1024) return f32 ? run_embed_grad<true, 2>(a, w, stream) : run_embed_grad<false, 2>(a, w, stream);
-  return f32 ? run_embed_grad<true, 4>(a, w, stream) : run_embed_grad<false, 4>(a, w, stream);
+  if (e != hipSuccess || a.rows == 0) return e;
+  return f32 ? run_embed_grad<true>(a, w, stream) : run_embed_grad<false>(a, w, stream);
 }
 
 }  // namespace dsr
