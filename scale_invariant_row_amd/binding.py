@@ -12,7 +12,9 @@ holding the bit patterns.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import re
 from typing import List, NamedTuple, Optional, Sequence, Tuple
@@ -88,7 +90,8 @@ class RescaleDesc(ctypes.Structure):
 
 
 _lib = None
-_token = False
+_token = None          # the library once ds_token_rows.h's entry points are declared
+_raw_stream = None     # torch's own look-up of a device's current stream, where it has one
 
 
 def lib() -> ctypes.CDLL:
@@ -142,9 +145,9 @@ def lib() -> ctypes.CDLL:
 def _token_lib() -> ctypes.CDLL:
     """The library with ds_token_rows.h's entry points declared; raises if the
     loaded build does not hold them."""
-    global _token
-    L = lib()
-    if not _token:
+    global _token, _raw_stream
+    if _token is None:
+        L = lib()
         vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
         sig = {
             "ds_embed_rows": [vp, i32, i64, vp, i32, f32, vp, i64, i64, vp],
@@ -172,8 +175,9 @@ def _token_lib() -> ctypes.CDLL:
                     raise RuntimeError(f"{LIB_PATH} does not hold {name}: build the library again "
                                        "with `python -m scale_invariant_row_amd.build`") from None
                 f.argtypes, f.restype = args, res
-        _token = True
-    return L
+        _raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+        _token = L
+    return _token
 
 
 def header_functions(header: str = HEADER) -> List[str]:
@@ -198,9 +202,15 @@ def _check(status: int, what: str) -> None:
 
 # --------------------------------------------------------------- tensors
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _bf16_2d(t, name, device: bool = True):
@@ -671,24 +681,42 @@ def ds_rescale_after_step(ws: Sequence, moms: Optional[Sequence] = None,
 
 # ------------------------------------------------------------- token rows
 
+# Calls of a few rows take less time on the GPU than in here, so the common
+# case (the tensors' device is the current one, its current stream) enters no
+# context, and sizes are asked for once.
+
+_SAME = contextlib.nullcontext()
+
+
 def _launch_on(t, stream):
-    """Contexts of a call on tensor t: its device, and the launch stream as
-    torch's current one, so what is allocated inside belongs to that stream."""
+    """(context, raw stream) of a call on tensor t: inside the context t's
+    device is the current one and the launch stream torch's current one, so
+    what is allocated there belongs to that stream."""
     torch = _torch()
-    import contextlib
+    if stream is None:
+        index = t.get_device()
+        raw = torch.cuda.current_stream(index).cuda_stream if _raw_stream is None \
+            else _raw_stream(index)
+        return (_SAME if torch.cuda.current_device() == index else torch.cuda.device(index)), raw
+    s = _torch_stream(t, stream)
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(t.device))
-    if stream is not None:
-        ctx.enter_context(torch.cuda.stream(_torch_stream(t, stream)))
-    return ctx
+    ctx.enter_context(torch.cuda.stream(s))
+    return ctx, s.cuda_stream
 
 
-def _workspace(nbytes: int, what: str, device):
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(call: str, *sizes) -> int:
+    n = getattr(_token_lib(), call + "_workspace")(*sizes)
+    if n < 0:
+        _check(n, call)
+    return n
+
+
+def _workspace(nbytes: int, like):
     """Scratch memory of a call, on the launch stream: dropped after the call,
     its block is handed only to work ordered after the call's kernels."""
-    if nbytes < 0:
-        _check(nbytes, what)
-    return _torch().empty(nbytes, dtype=_torch().uint8, device=device) if nbytes else None
+    return like.new_empty(nbytes, dtype=_torch().uint8) if nbytes else None
 
 
 def _ptr(t):
@@ -706,24 +734,26 @@ def _value_type(t, name: str) -> int:
 
 def _ids(t, name: str, rows: Optional[int] = None) -> int:
     torch = _torch()
-    if t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 or not t.is_contiguous() \
+    wide = t.dtype == torch.int64
+    if not (wide or t.dtype == torch.int32) or t.dim() != 1 or not t.is_contiguous() \
             or (rows is not None and t.shape[0] != rows):
         want = "[rows]" if rows is None else f"[{rows}]"
         raise ValueError(f"{name}: expected a contiguous int32 or int64 {want} tensor")
-    return 8 if t.dtype == torch.int64 else 4
+    return 8 if wide else 4
 
 
-def _vec(t, name: str, n: int, dtype=None):
-    dtype = _torch().float32 if dtype is None else dtype
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous()):
+def _vec(t, name: str, n: int, dtype):
+    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != n
+                          or not t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous {dtype} [{n}] tensor")
 
 
-def _on_device_of(first, name: str, others):
-    if first.device.type != "cuda":
+def _on_device_of(first, name: str, **others):
+    if not first.is_cuda:
         raise ValueError(f"{name}: must be on a HIP device")
-    for t, n in others:
-        if t is not None and t.device != first.device:
+    index = first.get_device()
+    for n, t in others.items():
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{n}: must be on the HIP device of {name}")
 
 
@@ -743,13 +773,14 @@ def ds_embed_rows(table, ids, scale: float = 1.0, out=None, stream=None):
         _bf16_2d(out, "out", device=False)
         if tuple(out.shape) != (rows, cols):
             raise ValueError(f"out: expected [{rows}, {cols}]")
-    _on_device_of(table, "table", [(ids, "ids"), (out, "out")])
-    with _launch_on(table, stream):
+    _on_device_of(table, "table", ids=ids, out=out)
+    L = _token_lib()
+    ctx, raw = _launch_on(table, stream)
+    with ctx:
         if out is None:
-            out = torch.empty(rows, cols, dtype=torch.bfloat16, device=table.device)
-        st = _token_lib().ds_embed_rows(table.data_ptr(), kind, vocab, ids.data_ptr(), id_bytes,
-                                        float(scale), out.data_ptr(), rows, cols,
-                                        _stream_of(table, stream))
+            out = table.new_empty((rows, cols), dtype=torch.bfloat16)
+        st = L.ds_embed_rows(table.data_ptr(), kind, vocab, ids.data_ptr(), id_bytes, scale,
+                             out.data_ptr(), rows, cols, raw)
     _check(st, "ds_embed_rows")
     return out
 
@@ -780,17 +811,18 @@ def ds_embed_rows_backward(dy, ids, vocab: int, scale: float = 1.0, dtable=None,
         raise ValueError("dtable: accumulate needs one")
     elif dtype not in (None, torch.float32, torch.bfloat16):
         raise TypeError(f"dtype: expected fp32 or bf16, got {dtype}")
-    _on_device_of(dy, "dy", [(ids, "ids"), (dtable, "dtable")])
+    _on_device_of(dy, "dy", ids=ids, dtable=dtable)
     L = _token_lib()
-    with _launch_on(dy, stream):
+    nbytes = _workspace_bytes("ds_embed_rows_backward", vocab, rows, cols)
+    ctx, raw = _launch_on(dy, stream)
+    with ctx:
         if dtable is None:
-            dtable = torch.empty(vocab, cols, dtype=dtype or torch.float32, device=dy.device)
-        nbytes = L.ds_embed_rows_backward_workspace(vocab, rows, cols)
-        ws = _workspace(nbytes, "ds_embed_rows_backward", dy.device)
-        st = L.ds_embed_rows_backward(dy.data_ptr(), ids.data_ptr(), id_bytes, float(scale),
+            dtable = dy.new_empty((vocab, cols), dtype=dtype or torch.float32)
+        ws = _workspace(nbytes, dy)
+        st = L.ds_embed_rows_backward(dy.data_ptr(), ids.data_ptr(), id_bytes, scale,
                                       dtable.data_ptr(), _value_type(dtable, "dtable"),
                                       int(bool(accumulate)), vocab, rows, cols, _ptr(ws), nbytes,
-                                      _stream_of(dy, stream))
+                                      raw)
     _check(st, "ds_embed_rows_backward")
     return dtable
 
@@ -809,7 +841,10 @@ def _heads(t, name: str, head_dim: int, rows: Optional[int] = None) -> int:
 
 
 def _row_stride(t) -> int:
-    """A view's row stride; a lone row's may be anything, and is not read."""
+    """A view's row stride (0 for None); a lone row's may be anything, and is
+    not read."""
+    if t is None:
+        return 0
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
 
 
@@ -820,9 +855,9 @@ def _qk_rms_checks(q, k, positions, inv_freq, q_weight, k_weight, head_dim):
     nq = _heads(q, "q", head_dim)
     nk = _heads(k, "k", head_dim, q.shape[0]) if k is not None else 0
     _vec(positions, "positions", q.shape[0], torch.int32)
-    _vec(inv_freq, "inv_freq", head_dim // 2)
-    _vec(q_weight, "q_weight", head_dim)
-    _vec(k_weight, "k_weight", head_dim)
+    _vec(inv_freq, "inv_freq", head_dim // 2, torch.float32)
+    _vec(q_weight, "q_weight", head_dim, torch.float32)
+    _vec(k_weight, "k_weight", head_dim, torch.float32)
     return nq, nk
 
 
@@ -852,19 +887,19 @@ def ds_qk_rows_rms(q, k, positions, inv_freq, q_weight, k_weight, head_dim: int,
     rows = q.shape[0]
     _like_heads(q_out, q, "q_out", head_dim, rows, nq)
     _like_heads(k_out, k, "k_out", head_dim, rows, nk)
-    _on_device_of(q, "q", [(k, "k"), (positions, "positions"), (inv_freq, "inv_freq"),
-                           (q_weight, "q_weight"), (k_weight, "k_weight"), (q_out, "q_out"),
-                           (k_out, "k_out")])
-    with _launch_on(q, stream):
+    _on_device_of(q, "q", k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
+                  k_weight=k_weight, q_out=q_out, k_out=k_out)
+    L = _token_lib()
+    ctx, raw = _launch_on(q, stream)
+    with ctx:
         if q_out is None:
-            q_out = torch.empty(rows, nq * head_dim, dtype=q.dtype, device=q.device)
+            q_out = q.new_empty((rows, nq * head_dim))
         if k is not None and k_out is None:
-            k_out = torch.empty(rows, nk * head_dim, dtype=k.dtype, device=k.device)
-        ld = lambda t: 0 if t is None else _row_stride(t)  # noqa: E731
-        st = _token_lib().ds_qk_rows_rms(
-            q.data_ptr(), ld(q), _ptr(k), ld(k), positions.data_ptr(), inv_freq.data_ptr(),
-            _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(), ld(q_out), _ptr(k_out), ld(k_out),
-            rows, nq, nk, head_dim, float(eps), _stream_of(q, stream))
+            k_out = k.new_empty((rows, nk * head_dim))
+        st = L.ds_qk_rows_rms(
+            q.data_ptr(), _row_stride(q), _ptr(k), _row_stride(k), positions.data_ptr(),
+            inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(),
+            _row_stride(q_out), _ptr(k_out), _row_stride(k_out), rows, nq, nk, head_dim, eps, raw)
     _check(st, "ds_qk_rows_rms")
     return q_out, k_out
 
@@ -887,28 +922,28 @@ def ds_qk_rows_rms_backward(q, k, positions, inv_freq, q_weight, k_weight, dq_ou
     _like_heads(dk_out, k, "dk_out", head_dim, rows, nk)
     _like_heads(dq, q, "dq", head_dim, rows, nq)
     _like_heads(dk, k, "dk", head_dim, rows, nk)
-    _on_device_of(q, "q", [(k, "k"), (positions, "positions"), (inv_freq, "inv_freq"),
-                           (q_weight, "q_weight"), (k_weight, "k_weight"), (dq_out, "dq_out"),
-                           (dk_out, "dk_out"), (dq, "dq"), (dk, "dk")])
+    _on_device_of(q, "q", k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight,
+                  k_weight=k_weight, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk)
     L = _token_lib()
-    with _launch_on(q, stream):
+    nbytes = _workspace_bytes("ds_qk_rows_rms_backward", rows, nq, nk, head_dim) \
+        if want_dweights else 0
+    ctx, raw = _launch_on(q, stream)
+    with ctx:
         if dq is None:
-            dq = torch.empty(rows, nq * head_dim, dtype=q.dtype, device=q.device)
+            dq = q.new_empty((rows, nq * head_dim))
         if k is not None and dk is None:
-            dk = torch.empty(rows, nk * head_dim, dtype=k.dtype, device=k.device)
-        dqw = dkw = ws = None
-        nbytes = 0
+            dk = k.new_empty((rows, nk * head_dim))
+        dqw = dkw = None
         if want_dweights:
-            dqw = torch.empty(head_dim, dtype=torch.float32, device=q.device)
-            dkw = torch.empty_like(dqw) if k is not None else None
-            nbytes = L.ds_qk_rows_rms_backward_workspace(rows, nq, nk, head_dim)
-            ws = _workspace(nbytes, "ds_qk_rows_rms_backward", q.device)
-        ld = lambda t: 0 if t is None else _row_stride(t)  # noqa: E731
+            dqw = q.new_empty(head_dim, dtype=torch.float32)
+            dkw = q.new_empty(head_dim, dtype=torch.float32) if k is not None else None
+        ws = _workspace(nbytes, q)
         st = L.ds_qk_rows_rms_backward(
-            q.data_ptr(), ld(q), _ptr(k), ld(k), positions.data_ptr(), inv_freq.data_ptr(),
-            _ptr(q_weight), _ptr(k_weight), dq_out.data_ptr(), ld(dq_out), _ptr(dk_out), ld(dk_out),
-            dq.data_ptr(), ld(dq), _ptr(dk), ld(dk), _ptr(dqw), _ptr(dkw), rows, nq, nk, head_dim,
-            float(eps), _ptr(ws), nbytes, _stream_of(q, stream))
+            q.data_ptr(), _row_stride(q), _ptr(k), _row_stride(k), positions.data_ptr(),
+            inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight), dq_out.data_ptr(),
+            _row_stride(dq_out), _ptr(dk_out), _row_stride(dk_out), dq.data_ptr(), _row_stride(dq),
+            _ptr(dk), _row_stride(dk), _ptr(dqw), _ptr(dkw), rows, nq, nk, head_dim, eps, _ptr(ws),
+            nbytes, raw)
     _check(st, "ds_qk_rows_rms_backward")
     return dq, dk, dqw, dkw
 
@@ -944,25 +979,26 @@ def ds_logprob_rows(logits, labels=None, scale=None, inv_temp: float = 1.0, top_
     torch = _torch()
     kind, rows, vocab, ld = _logits(logits, "logits")
     label_bytes = 8 if labels is None else _ids(labels, "labels", rows)
-    _vec(scale, "scale", vocab)
+    _vec(scale, "scale", vocab, torch.float32)
     top_k = int(top_k)
     if not 0 <= top_k <= min(DS_MAX_TOP, vocab):
         raise ValueError(f"top_k: expected 0 to {min(DS_MAX_TOP, vocab)}")
-    _on_device_of(logits, "logits", [(labels, "labels"), (scale, "scale")])
+    _on_device_of(logits, "logits", labels=labels, scale=scale)
     L = _token_lib()
-    with _launch_on(logits, stream):
-        new = lambda *shape, dtype=torch.float32: torch.empty(  # noqa: E731
-            *shape, dtype=dtype, device=logits.device)
-        logp = new(rows) if labels is not None else None
-        entropy, lse = new(rows), new(rows)
-        ids = new(rows, top_k, dtype=torch.int32) if top_k else None
-        top = new(rows, top_k) if top_k else None
-        nbytes = L.ds_logprob_rows_workspace(rows, vocab, top_k)
-        ws = _workspace(nbytes, "ds_logprob_rows", logits.device)
-        st = L.ds_logprob_rows(logits.data_ptr(), kind, ld, _ptr(scale), float(inv_temp),
-                               _ptr(labels), label_bytes, _ptr(logp), entropy.data_ptr(),
-                               lse.data_ptr(), _ptr(ids), _ptr(top), top_k, rows, vocab, _ptr(ws),
-                               nbytes, _stream_of(logits, stream))
+    nbytes = _workspace_bytes("ds_logprob_rows", rows, vocab, top_k)
+    ctx, raw = _launch_on(logits, stream)
+    with ctx:
+        lse, entropy, logp = logits.new_empty((3, rows), dtype=torch.float32).unbind()
+        if labels is None:
+            logp = None
+        ids = top = None
+        if top_k:
+            ids = logits.new_empty((rows, top_k), dtype=torch.int32)
+            top = logits.new_empty((rows, top_k), dtype=torch.float32)
+        ws = _workspace(nbytes, logits)
+        st = L.ds_logprob_rows(logits.data_ptr(), kind, ld, _ptr(scale), inv_temp, _ptr(labels),
+                               label_bytes, _ptr(logp), entropy.data_ptr(), lse.data_ptr(),
+                               _ptr(ids), _ptr(top), top_k, rows, vocab, _ptr(ws), nbytes, raw)
     _check(st, "ds_logprob_rows")
     return LogprobRows(logp, entropy, lse, ids, top)
 
@@ -987,29 +1023,27 @@ def ds_logprob_rows_backward(logits, labels, lse, entropy, dlogp, dentropy=None,
     if lse is None:
         raise ValueError("lse: the forward call's is needed")
     for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
-        _vec(t, n, rows)
-    _vec(scale, "scale", vocab)
+        _vec(t, n, rows, torch.float32)
+    _vec(scale, "scale", vocab, torch.float32)
     ldo = vocab
     if dlogits is not None:
         if dlogits.dtype != logits.dtype or tuple(dlogits.shape) != (rows, vocab):
             raise ValueError(f"dlogits: expected a [{rows}, {vocab}] tensor like logits")
         ldo = _logits(dlogits, "dlogits")[3]
-    _on_device_of(logits, "logits", [(labels, "labels"), (lse, "lse"), (entropy, "entropy"),
-                                     (dlogp, "dlogp"), (dentropy, "dentropy"), (scale, "scale"),
-                                     (dlogits, "dlogits")])
+    _on_device_of(logits, "logits", labels=labels, lse=lse, entropy=entropy, dlogp=dlogp,
+                  dentropy=dentropy, scale=scale, dlogits=dlogits)
     L = _token_lib()
-    with _launch_on(logits, stream):
+    want_dscale = scale is not None and want_dscale
+    nbytes = _workspace_bytes("ds_logprob_rows_backward", rows, vocab) if want_dscale else 0
+    ctx, raw = _launch_on(logits, stream)
+    with ctx:
         if dlogits is None:
-            dlogits = torch.empty(rows, vocab, dtype=logits.dtype, device=logits.device)
-        dscale = ws = None
-        nbytes = 0
-        if scale is not None and want_dscale:
-            dscale = torch.empty(vocab, dtype=torch.float32, device=logits.device)
-            nbytes = L.ds_logprob_rows_backward_workspace(rows, vocab)
-            ws = _workspace(nbytes, "ds_logprob_rows_backward", logits.device)
+            dlogits = logits.new_empty((rows, vocab))
+        dscale = logits.new_empty(vocab, dtype=torch.float32) if want_dscale else None
+        ws = _workspace(nbytes, logits)
         st = L.ds_logprob_rows_backward(
-            logits.data_ptr(), kind, ld, _ptr(scale), float(inv_temp), _ptr(labels), label_bytes,
+            logits.data_ptr(), kind, ld, _ptr(scale), inv_temp, _ptr(labels), label_bytes,
             lse.data_ptr(), _ptr(entropy), _ptr(dlogp), _ptr(dentropy), dlogits.data_ptr(), ldo,
-            _ptr(dscale), rows, vocab, _ptr(ws), nbytes, _stream_of(logits, stream))
+            _ptr(dscale), rows, vocab, _ptr(ws), nbytes, raw)
     _check(st, "ds_logprob_rows_backward")
     return dlogits, dscale

@@ -43,6 +43,19 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
+// Sum over the lanes at the same place of the wave's 64 / LPH heads: rotations
+// within 16 lanes, then the swaps across them.
+template <int LPH>
+__device__ __forceinline__ float heads_sum(float v) {
+  if constexpr (LPH <= 1) v = v + dpp_f<0x121>(v);       // row_ror:1
+  if constexpr (LPH <= 2) v = v + dpp_f<0x122>(v);
+  if constexpr (LPH <= 4) v = v + dpp_f<0x124>(v);
+  if constexpr (LPH <= 8) v = v + dpp_f<0x128>(v);
+  f32x2_t p = swap16(v);
+  p = swap32(p.x + p.y);
+  return p.x + p.y;
+}
+
 __device__ __forceinline__ void unpack8(u32x4_t t, float* v) {
   v[0] = bf_lo(t.x); v[1] = bf_hi(t.x); v[2] = bf_lo(t.y); v[3] = bf_hi(t.y);
   v[4] = bf_lo(t.z); v[5] = bf_hi(t.z); v[6] = bf_lo(t.w); v[7] = bf_hi(t.w);
@@ -315,8 +328,7 @@ __global__ void __launch_bounds__(256, 4) qk_rows_rms_backward_kernel(const QkRm
   for (int which = 0; which < 2; ++which)
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      float t = dw[which][j];
-      for (int d = LPH; d < 64; d *= 2) t = t + __shfl_xor(t, d);   // heads of the wave step
+      const float t = heads_sum<LPH>(dw[which][j]);       // over the heads of the wave step
       if (hs == 0 && active) part[wave][which][(j < 8 ? 0 : half) + at + j % 8] = t;
     }
   __syncthreads();
