@@ -18,8 +18,8 @@
 // time their 2.1 GB take from memory.
 //
 // Masked tokens (z = -inf) have exp 0 but 0 * -inf in T.  The fast sums go
-// without a test for them: a chunk whose sums come out NaN, or that holds
-// nothing above -inf, is summed again in the careful form (lp_careful), where
+// without a test for them: a chunk whose sums come out NaN, or past 2^20, or
+// that holds nothing above -inf, is summed again in the careful form (lp_careful), where
 // the factor is clamped at -200 (exp is 0 there already); a NaN of the row's
 // own stays NaN.
 #include <algorithm>
@@ -236,8 +236,10 @@ __device__ __forceinline__ void lp_load_scale(float (&sc)[kLpPer], const float* 
   }
 }
 
-// S and T about base with every step guarded: see the head of this file.
-__device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float M) {
+// S and T about the chunk's maximum with every step guarded: see the head of
+// this file.  m: the lane's maximum.
+__device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float m) {
+  const float M = wave_max(m);
   const float base = M == -__builtin_inff() ? 0.f : M;
   float S = 0.f, T = 0.f;
 #pragma unroll
@@ -249,11 +251,16 @@ __device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float M) {
   return LpSum{M, wave_sum(S), wave_sum(T)};
 }
 
-// A chunk's sums, the same in every lane.  With c = fp32(M log2 e) the fast
-// form sums about c in log2 units, z log2 e - c one fused multiply-add; r, the
-// rounding error of c (a fused multiply-add gives it exactly), turns the sums
-// into those about M:  z log2 e - c = (z - M) log2 e + r.
-__device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float M) {
+// A chunk's sums, the same in every lane.  Any base near the maximum will do,
+// and lane 0's maximum needs no exchange; where the chunk reaches so far above
+// it that S passes 2^20 (and log S and T / S would lose digits to each other),
+// the careful form takes over.  With c = fp32(M log2 e) the sums
+// are about c in log2 units, z log2 e - c one fused multiply-add; r, the
+// rounding error of c (a fused multiply-add gives it exactly), turns them into
+// those about M:  z log2 e - c = (z - M) log2 e + r.
+__device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float m) {
+  const float M = __builtin_bit_cast(
+      float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, m)));
   const float c = M * kLog2e;
   float S = 0.f, T = 0.f;
 #pragma unroll
@@ -264,14 +271,13 @@ __device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float M)
   }
   S = wave_sum(S);
   T = wave_sum(T);
-  if (!(S < __builtin_inff() && T == T)) return lp_careful(z, M);      // uniform
+  if (!(S < 0x1p20f && T == T)) return lp_careful(z, m);               // uniform
   const float r = __builtin_fmaf(M, kLog2e, -c);
   const float f = __builtin_amdgcn_exp2f(-r);
   return LpSum{M, S * f, (T - r * S) * f * kLn2};
 }
 
-// Row r of a workgroup's rows, one of `waves` waves that share them: the
-// chunks first, first + waves, ...
+// A wave's share of a row: the sums of one chunk at a time, and the list.
 template <bool F32, bool SCALED>
 struct LpRow {
   LpTop top;
@@ -279,8 +285,8 @@ struct LpRow {
   __device__ __forceinline__ LpSum chunk(const LpRaw<F32>& raw, const float (&sc)[kLpPer],
                                          float inv_temp, int c0, int top_k, int lane) {
     using R = LpRaw<F32>;
-    float z[kLpPer];
-    float m = -__builtin_inff();
+    constexpr int G = 8;                              // values of a group
+    float z[kLpPer], gm[kLpPer / G];                  // and the groups' maxima
 #pragma unroll
     for (int i = 0; i < kLpPer; ++i) {
       z[i] = raw.at(i);
@@ -290,25 +296,37 @@ struct LpRow {
 #pragma unroll
       for (int i = 0; i < kLpPer; ++i) z[i] = z[i] * inv_temp;
     }
+    float m = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < kLpPer; ++i) m = fmaxf(m, z[i]);
-    const LpSum s = lp_chunk_sum(z, wave_max(m));
+    for (int g = 0; g < kLpPer / G; ++g) {
+      gm[g] = z[g * G];
+#pragma unroll
+      for (int i = 1; i < G; ++i) gm[g] = fmaxf(gm[g], z[g * G + i]);
+      m = fmaxf(m, gm[g]);
+    }
+    const LpSum s = lp_chunk_sum(z, m);
     if (top_k > 0) {
-      const float kz = top.kth != 0 ? lp_unorder((uint32_t)(top.kth >> 32)) : -__builtin_inff();
-      const uint64_t hits = __builtin_amdgcn_ballot_w64(m > kz);
+      // the least z that can enter the list: above the k-th best so far
+      // (columns only rise, so an equal value comes too late)
+      uint32_t least = top.kth != 0 ? (uint32_t)(top.kth >> 32) + 1 : lp_order(-__builtin_inff()) + 1;
+      const uint64_t hits = __builtin_amdgcn_ballot_w64(m >= lp_unorder(least));
       if (hits != 0) {
         // many lanes: only values that reach the k-th largest lane maximum
         // can be among the chunk's k best
-        float least = -__builtin_inff();
         if (__builtin_popcountll(hits) > top_k) {
           const uint32_t t = lp_kth_lane(m > -__builtin_inff() ? lp_order(m) : 0u, top_k);
-          if (t != 0) least = lp_unorder(t);
+          least = t > least ? t : least;
         }
+        const float lz = lp_unorder(least);
 #pragma unroll
-        for (int i = 0; i < kLpPer; ++i) {
-          const bool may = z[i] > kz && z[i] >= least;
-          if (__builtin_amdgcn_ballot_w64(may) != 0)
-            top.add(may ? lp_key(z[i], R::col(c0, i / R::VE, lane) + i % R::VE) : 0, top_k, lane);
+        for (int g = 0; g < kLpPer / G; ++g) {
+          if (__builtin_amdgcn_ballot_w64(gm[g] >= lz) == 0) continue;
+#pragma unroll
+          for (int i = g * G; i < (g + 1) * G; ++i) {
+            const bool may = z[i] >= lz;
+            if (__builtin_amdgcn_ballot_w64(may) != 0)
+              top.add(may ? lp_key(z[i], R::col(c0, i / R::VE, lane) + i % R::VE) : 0, top_k, lane);
+          }
         }
       }
     }
@@ -354,25 +372,26 @@ __global__ void __launch_bounds__(256) logprob_rows_kernel(const LogprobArgs a, 
     y = lp_label(a.labels, a.label_bytes, row0 + wave, a.vocab);
     if (y >= 0) zy = lp_z(lp_load<F32>(a.x, (row0 + wave) * a.ld + y), a.scale, y, a.inv_temp);
   }
+  // a last workgroup of fewer rows works on its last one again
   LpRow<F32, SCALED> st[ROWS];
-  LpRaw<F32> raw;
-  if (wave < chunks) raw.load(a.x, row0 * a.ld, wave * kLpChunk, a.vocab, lane);
+  LpRaw<F32> raw[2];
+  auto load = [&](LpRaw<F32>& to, int r, int c) {
+    if (c < chunks) to.load(a.x, (row0 + (r < rows ? r : rows - 1)) * a.ld, c * kLpChunk, a.vocab, lane);
+  };
+  load(raw[0], 0, wave);
   for (int c = wave; c < chunks; c += 4) {
     float sc[kLpPer];
     if constexpr (SCALED) lp_load_scale<F32>(sc, a.scale, c * kLpChunk, a.vocab, lane);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      if (r >= rows) break;                           // uniform
-      const LpRaw<F32> now = raw;
-      const bool last = r + 1 >= rows;
-      const int nc = last ? c + 4 : c;
-      if (nc < chunks)
-        raw.load(a.x, (row0 + (last ? 0 : r + 1)) * a.ld, nc * kLpChunk, a.vocab, lane);
+      LpRaw<F32>&now = raw[r % 2], &next = raw[(r + 1) % 2];
+      load(next, r + 1 < ROWS ? r + 1 : 0, r + 1 < ROWS ? c : c + 4);
       const LpSum s = st[r].chunk(now, sc, a.inv_temp, c * kLpChunk, a.top_k, lane);
       if (lane == 0) {
         float* p = sums + ((int64_t)r * chunks + c) * 3;
         p[0] = s.M; p[1] = s.S; p[2] = s.T;
       }
+      if constexpr (ROWS == 1) raw[0] = raw[1];
     }
   }
   if (a.top_k > 0 && lane < a.top_k) {
@@ -422,28 +441,45 @@ logprob_split_kernel(const LogprobArgs a, int chunks, int splits, float* sums, u
 }
 
 // Joins a split row: one wave per row.  The lists are sorted, so once no wave
-// has a place-j key for the list, deeper ones have none either.
+// of 64 has a place-j key for the list, their deeper ones have none either.
 template <bool F32>
 __global__ void __launch_bounds__(64)
 logprob_join_kernel(const LogprobArgs a, int chunks, int waves, const float* sums,
                     const uint64_t* keys) {
+  constexpr int AT_ONCE = 8;                          // places of the lists loaded together
   const int lane = threadIdx.x;
   const int64_t row = blockIdx.x;
+  uint64_t k[AT_ONCE];
+  auto load = [&](int j0, int w0) {
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j)
+      k[j] = j0 + j < a.top_k && w0 + lane < waves
+                 ? keys[(row * a.top_k + j0 + j) * waves + w0 + lane] : 0;
+  };
+  load(0, 0);                                         // on its way during the sums
   const int y = lp_label(a.labels, a.label_bytes, row, a.vocab);
-  const float zy = y >= 0 ? lp_z(lp_load<F32>(a.x, row * a.ld + y), a.scale, y, a.inv_temp) : 0.f;
   const LpSum sum = lp_join_all(chunks, lane, [&](int c) {
     const float* p = sums + (row * chunks + c) * 3;
     return LpSum{p[0], p[1], p[2]};
   });
+  const float zy = y >= 0 ? lp_z(lp_load<F32>(a.x, row * a.ld + y), a.scale, y, a.inv_temp) : 0.f;
   LpTop top;
-  for (int j = 0; j < a.top_k; ++j) {
+  for (int j0 = 0; j0 < a.top_k; j0 += AT_ONCE) {
     uint64_t any = 0;
     for (int w0 = 0; w0 < waves; w0 += 64) {
-      const uint64_t k = w0 + lane < waves ? keys[(row * a.top_k + j) * waves + w0 + lane] : 0;
-      any |= __builtin_amdgcn_ballot_w64(k > top.kth);
-      top.add(k, a.top_k, lane);
+      if (j0 > 0 || w0 > 0) load(j0, w0);
+      // as in a chunk: only keys that reach the k-th largest first place
+      uint32_t least = 0;
+      if (j0 == 0 && w0 == 0) least = lp_kth_lane((uint32_t)(k[0] >> 32), a.top_k);
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) {
+        const uint64_t in = (uint32_t)(k[j] >> 32) >= least ? k[j] : 0;
+        any = __builtin_amdgcn_ballot_w64(in > top.kth);
+        if (any == 0) break;                          // uniform: deeper places hold less
+        top.add(in, a.top_k, lane);
+      }
     }
-    if (any == 0) break;
+    if (waves <= 64 && any == 0) break;
   }
   lp_write_row(a, row, sum, top.key, y, zy, lane);
 }
@@ -554,15 +590,23 @@ __device__ __forceinline__ LpRowGrad lp_row_grad(const LogprobGradArgs& a, int64
 
 constexpr int kLpTileRows = 128;                      // most rows of a tile
 
-template <bool F32>
-struct LpVec {                                        // a thread's 16 bytes
+// A thread's 16 bytes.  STREAM: the logits do not fit the last-level cache, so
+// their loads are non-temporal (869 against 885 us for 4.3 GB in and out);
+// smaller ones are read through it, where their producer left them (15.0
+// against 18.0 us for 65 MB).  Stores are non-temporal either way (a cached
+// store: 19.5 us).
+template <bool F32, bool STREAM>
+struct LpVec {
   static constexpr int VE = F32 ? 4 : 8;
   using V = typename std::conditional<F32, u32x4_a4, u32x4_a2>::type;
   using E = typename std::conditional<F32, uint32_t, uint16_t>::type;
 
   static __device__ __forceinline__ u32x4_t load(const void* x, int64_t at, int c, int vocab) {
     const E* p = static_cast<const E*>(x) + at + c;
-    if (c + VE <= vocab) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+    if (c + VE <= vocab) {
+      if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+      else return *reinterpret_cast<const V*>(p);
+    }
     uint32_t e[VE];
 #pragma unroll
     for (int k = 0; k < VE; ++k) e[k] = c + k < vocab ? (uint32_t)p[k] : 0u;
@@ -597,10 +641,10 @@ struct LpVec {                                        // a thread's 16 bytes
   }
 };
 
-template <bool F32, bool SCALED>
+template <bool F32, bool SCALED, bool STREAM>
 __global__ void __launch_bounds__(256)
 logprob_grad_kernel(const LogprobGradArgs a, int strips, int tile_rows, float* parts) {
-  using L = LpVec<F32>;
+  using L = LpVec<F32, STREAM>;
   constexpr int VE = L::VE, AHEAD = 4;
   __shared__ LpRowGrad rg[kLpTileRows];
   const int64_t tile = blockIdx.x / strips;
@@ -692,6 +736,7 @@ template <bool F32, bool SCALED>
 static hipError_t run_logprob_grad(const LogprobGradArgs& a, float* parts, hipStream_t stream) {
   const int strips = lp_strips(F32, a.vocab), t = lp_tile_rows(a.rows, a.vocab);
   const int64_t tiles = (a.rows + t - 1) / t;
+  const bool large = a.rows * a.vocab > (256 << 20) / (F32 ? 8 : 4);   // in and out: 256 MiB
   // launches of at most 2^20 tiles' strips (a grid's limit is 2^31 threads)
   const int64_t most = std::max<int64_t>(1, (1 << 20) / strips);
   for (int64_t t0 = 0; t0 < tiles; t0 += most) {
@@ -705,8 +750,11 @@ static hipError_t run_logprob_grad(const LogprobGradArgs& a, float* parts, hipSt
     if (a.entropy != nullptr) p.entropy = a.entropy + r0;
     if (a.dlogp != nullptr) p.dlogp = a.dlogp + r0;
     if (a.dentropy != nullptr) p.dentropy = a.dentropy + r0;
-    logprob_grad_kernel<F32, SCALED><<<(int)(n * strips), 256, 0, stream>>>(
-        p, strips, t, parts != nullptr ? parts + t0 * a.vocab : nullptr);
+    float* to = parts != nullptr ? parts + t0 * a.vocab : nullptr;
+    if (large)
+      logprob_grad_kernel<F32, SCALED, true><<<(int)(n * strips), 256, 0, stream>>>(p, strips, t, to);
+    else
+      logprob_grad_kernel<F32, SCALED, false><<<(int)(n * strips), 256, 0, stream>>>(p, strips, t, to);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
