@@ -15,7 +15,8 @@
 // Cost per value beside its load: unpack, scale, half a maximum, one fused
 // multiply-add to log2 units, exp2 (four issue slots), a sum and a fused
 // multiply-add: 10 slots, 270 us for 8,192 x 131,072 bf16 values, under the
-// time their 2.1 GB take from memory.
+// time their 2.1 GB take from memory.  Measured: 402 us (5.3 TB/s) with the 5
+// best of each row.
 //
 // Masked tokens (z = -inf) have exp 0 but 0 * -inf in T.  The fast sums go
 // without a test for them: a chunk whose sums come out NaN, or past 2^20, or
@@ -354,9 +355,10 @@ __device__ __forceinline__ void lp_write_row(const LogprobArgs& a, int64_t row, 
 }
 
 // One workgroup of four waves per ROWS rows.  Each wave takes every fourth
-// chunk of all of them, so a chunk's scale is loaded once for ROWS rows; the
-// next row's values are on their way while one is summed.  Dynamic LDS: the
-// chunks' sums, [ROWS][chunks].
+// chunk of all of them, so a chunk's scale is loaded once for ROWS rows (with
+// two rows 8,192 x 131,072 scaled bf16 took 457 us where four took 434); the
+// next row's values are on their way while one is summed (ROWS is 1 or even:
+// two buffers take turns).  Dynamic LDS: the chunks' sums, [ROWS][chunks].
 template <bool F32, bool SCALED, int ROWS>
 __global__ void __launch_bounds__(256) logprob_rows_kernel(const LogprobArgs a, int chunks) {
   extern __shared__ float sums[];
@@ -561,7 +563,10 @@ hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace,
 // columns (16 bytes a thread) down a tile of rows, so a column's scale is
 // loaded, and its gradient summed, once per tile; the tiles' sums go to the
 // workspace and are added in order by a second kernel.  What a row needs is
-// folded into five numbers in LDS:  d = p (gh lp + c), lp = z - lse.
+// folded into five numbers in LDS:  d = p (gh lp + c), lp = z - lse.  Bound by
+// memory: 8,192 x 131,072 bf16 with dscale in 777 us (5.5 TB/s); eight rows
+// loaded together where the logits stream (786 us with four), four where they
+// come from the cache (15.5 against 16.8 us for 509 x 32,003).
 //
 // lp is clamped at -200, where p is 0, so that a masked token's 0 * inf does
 // not arise; c is NaN where lse is, so that row's NaN is kept.
@@ -588,7 +593,7 @@ __device__ __forceinline__ LpRowGrad lp_row_grad(const LogprobGradArgs& a, int64
   return r;
 }
 
-constexpr int kLpTileRows = 128;                      // most rows of a tile
+constexpr int kLpTileRows = 32;                       // most rows of a tile
 
 // A thread's 16 bytes.  STREAM: the logits do not fit the last-level cache, so
 // their loads are non-temporal (869 against 885 us for 4.3 GB in and out);
@@ -645,7 +650,7 @@ template <bool F32, bool SCALED, bool STREAM>
 __global__ void __launch_bounds__(256)
 logprob_grad_kernel(const LogprobGradArgs a, int strips, int tile_rows, float* parts) {
   using L = LpVec<F32, STREAM>;
-  constexpr int VE = L::VE, AHEAD = 4;
+  constexpr int VE = L::VE, AHEAD = STREAM ? 8 : 4;   // rows loaded together
   __shared__ LpRowGrad rg[kLpTileRows];
   const int64_t tile = blockIdx.x / strips;
   const int c0 = (int)(blockIdx.x % strips) * 256 * VE;
@@ -717,7 +722,9 @@ static int lp_strips(bool f32, int64_t vocab) {
   return (int)((vocab + w - 1) / w);
 }
 
-// Rows of a tile: 8 to 128, about 2,048 workgroups in all.  A rule of the
+// Rows of a tile: 8 to 32, about 2,048 workgroups in all.  (8,192 x 131,072
+// bf16: 777 us with tiles of 32, 820 with 16 or 64, 864 with 128 -- the
+// longer, the further apart the rows that are read at one time.)  A rule of the
 // sizes alone (the type's strip width aside: the narrower is taken for both),
 // so the order of dscale's sums is too.
 static int lp_tile_rows(int64_t rows, int64_t vocab) {
