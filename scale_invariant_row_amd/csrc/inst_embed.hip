@@ -82,7 +82,6 @@ constexpr int kSortCap = kSortBlock;                      // rows kept in LDS
 constexpr int kClearVectors = 8 * kSortThreads;           // cleared by a workgroup: 128 KiB
 constexpr int kSortBins = 2048;                           // most tokens of a group
 constexpr int kRun = 32;
-constexpr int kAhead = 16;                                // of them loaded at a time
 
 // The workspace: start[parts * bins + 1] (first sorted row of each token),
 // order[rows] and token[rows] (row and token in sorted order), parts of sums
@@ -288,7 +287,7 @@ embed_sort_kernel(const void* ids, int rows, int vocab, const EmbedSort w, u32x4
 // A wave's columns: VE a lane, 4 where the table is fp32 and 8 where it is
 // bf16, so that its stores cover 1 KiB without gaps (with 8 columns a lane,
 // non-temporal fp32 stores of alternate 16 bytes reached 2.3 TB/s).
-template <bool F32>
+template <bool F32, bool ACC>
 struct EmbedCols {
   static constexpr int VE = F32 ? 4 : 8;
   using Raw = typename std::conditional<F32, u32x2_t, u32x4_t>::type;   // of a row of dy
@@ -341,13 +340,13 @@ struct EmbedCols {
 #pragma unroll
     for (int j = 0; j < VE; ++j) d[j] = v[j] * a.scale;
     if constexpr (F32) {
-      if (a.accumulate) {
+      if constexpr (ACC) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] += __uint_as_float(old[j]);
       }
       table(a, t).st16(__builtin_bit_cast(u32x4_t, f32x4_t{d[0], d[1], d[2], d[3]}), c * 4);
     } else {
-      if (a.accumulate) {
+      if constexpr (ACC) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           d[2 * j] += bf_lo(old[j]);
@@ -361,18 +360,21 @@ struct EmbedCols {
   }
 };
 
-// Sums by blocks of 32 sorted rows: one wave per block and 64 VE columns, 16
-// loads in flight together.  The rows of a token that lies in the block
+// Sums by blocks of 32 sorted rows: one wave per block and 64 VE columns, all
+// its loads in flight together (half of them, where the table's old rows take
+// registers too).  The rows of a token that lies in the block
 // give its row of the table; of one that came from the block before, part 0
 // of the block; of one that only goes on into the next, part 1.
 //
-// Bound by memory: for 32,768 x 4,096 (0.43 GB read and written) 96 us.  Eight
-// loads at a time measured the same (98 us).  Waves that gathered all rows of
+// Bound by memory: for 32,768 x 4,096 (0.43 GB read and written) 96 us.  For
+// 1,021 x 768 rows the whole gradient takes 24.0 us with 32 loads together,
+// 24.6 with 16 and 25.5 with eight.  Waves that gathered all rows of
 // one token, four at a time, needed their whole runs of 32 summed by a launch
 // before (28 us) and took 83 us more, held up by the frequent tokens.
-template <bool F32>
+template <bool F32, bool ACC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedGradArgs a, const EmbedSort w, int tiles) {
-  using C = EmbedCols<F32>;
+  constexpr int kAhead = ACC ? kRun / 2 : kRun;          // rows loaded at a time
+  using C = EmbedCols<F32, ACC>;
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t block = wave / tiles;
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedGradArgs a, c
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
       if (j0 + j < n) x[j] = C::load(a, __builtin_amdgcn_readlane(row, j0 + j), c);
-    if (a.accumulate) {
+    if constexpr (ACC) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
         if (ends >> (j0 + j) & 1) old[j] = C::load_old(a, __builtin_amdgcn_readlane(tok, j0 + j), c);
@@ -422,10 +424,10 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedGradArgs a, c
 
 // Tokens that span blocks: the wave of the block that a token starts in adds
 // part 1 of it and part 0 of the blocks that follow, in order.
-template <bool F32>
+template <bool F32, bool ACC>
 __global__ void __launch_bounds__(256)
 embed_join_kernel(const EmbedGradArgs a, const EmbedSort w, int tiles) {
-  using C = EmbedCols<F32>;
+  using C = EmbedCols<F32, ACC>;
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t block = wave / tiles;
@@ -444,7 +446,7 @@ embed_join_kernel(const EmbedGradArgs a, const EmbedSort w, int tiles) {
   C acc{};
   acc.add_part(C::part(a, w, k, 1), c);
   typename C::Old old{};
-  if (a.accumulate) old = C::load_old(a, t, c);
+  if constexpr (ACC) old = C::load_old(a, t, c);
 #pragma unroll 8
   for (int b = k + 1; b <= last; ++b) acc.add_part(C::part(a, w, b, 0), c);
   acc.store(a, t, c, old);
@@ -476,15 +478,15 @@ int64_t embed_grad_workspace(int64_t vocab, int64_t rows, int64_t cols) {
   return bytes;
 }
 
-template <bool F32>
+template <bool F32, bool ACC>
 static hipError_t run_embed_grad(const EmbedGradArgs& a, const EmbedSort& w, hipStream_t stream) {
-  constexpr int W = 64 * EmbedCols<F32>::VE;
+  constexpr int W = 64 * EmbedCols<F32, ACC>::VE;
   const int tiles = (a.cols + W - 1) / W;
   const int64_t waves = ((int64_t)a.rows + kRun - 1) / kRun * tiles;
-  embed_sum_kernel<F32><<<(int)((waves + 3) / 4), 256, 0, stream>>>(a, w, tiles);
+  embed_sum_kernel<F32, ACC><<<(int)((waves + 3) / 4), 256, 0, stream>>>(a, w, tiles);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.rows <= kRun) return e;
-  embed_join_kernel<F32><<<(int)((waves + 3) / 4), 256, 0, stream>>>(a, w, tiles);
+  embed_join_kernel<F32, ACC><<<(int)((waves + 3) / 4), 256, 0, stream>>>(a, w, tiles);
   return hipGetLastError();
 }
 
@@ -501,7 +503,9 @@ hipError_t launch_embed_rows_backward(bool f32, bool wide_ids, const EmbedGradAr
     embed_sort_kernel<int32_t><<<grid, kSortThreads, 0, stream>>>(a.ids, a.rows, a.vocab, w, table, vectors);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.rows == 0) return e;
-  return f32 ? run_embed_grad<true>(a, w, stream) : run_embed_grad<false>(a, w, stream);
+  if (a.accumulate)
+    return f32 ? run_embed_grad<true, true>(a, w, stream) : run_embed_grad<false, true>(a, w, stream);
+  return f32 ? run_embed_grad<true, false>(a, w, stream) : run_embed_grad<false, false>(a, w, stream);
 }
 
 }  // namespace dsr
