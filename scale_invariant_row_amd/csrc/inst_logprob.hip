@@ -564,9 +564,9 @@ hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace,
 // loaded, and its gradient summed, once per tile; the tiles' sums go to the
 // workspace and are added in order by a second kernel.  What a row needs is
 // folded into five numbers in LDS:  d = p (gh lp + c), lp = z - lse.  Bound by
-// memory: 8,192 x 131,072 bf16 with dscale in 777 us (5.5 TB/s); eight rows
-// loaded together where the logits stream (786 us with four), four where they
-// come from the cache (15.5 against 16.8 us for 509 x 32,003).
+// memory: 8,192 x 131,072 bf16 with dscale in 801 us (5.4 TB/s; 777 on another
+// GPU); eight rows loaded together where the logits stream (844 us with four),
+// four where they come from the cache (15.5 against 16.8 us for 509 x 32,003).
 //
 // lp is clamped at -200, where p is 0, so that a masked token's 0 * inf does
 // not arise; c is NaN where lse is, so that row's NaN is kept.
@@ -663,7 +663,12 @@ logprob_grad_kernel(const LogprobGradArgs a, int strips, int tile_rows, float* p
   for (int k = 0; k < VE; ++k) sc[k] = SCALED && c + k < a.vocab ? a.scale[c + k] : 1.f;
   __syncthreads();
   if (c >= a.vocab) return;
-  for (int r0 = 0; r0 < rows; r0 += AHEAD) {
+  // whole tiles begin in turn at each of their groups of rows: workgroups that
+  // run side by side are then not all at the same address modulo a power of
+  // two (801 against 822 us for 8,192 x 131,072)
+  const int turn = rows == tile_rows ? (int)(tile % (rows / AHEAD)) * AHEAD : 0;
+  for (int q0 = 0; q0 < rows; q0 += AHEAD) {
+    const int r0 = q0 + turn < rows ? q0 + turn : q0 + turn - rows;
     u32x4_t t[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
@@ -723,8 +728,7 @@ static int lp_strips(bool f32, int64_t vocab) {
 }
 
 // Rows of a tile: 8 to 32, about 2,048 workgroups in all.  (8,192 x 131,072
-// bf16: 777 us with tiles of 32, 820 with 16 or 64, 864 with 128 -- the
-// longer, the further apart the rows that are read at one time.)  A rule of the
+// bf16 on one GPU: 777 us with tiles of 32, 820 with 16 or 64; 864 with 128.)  A rule of the
 // sizes alone (the type's strip width aside: the narrower is taken for both),
 // so the order of dscale's sums is too.
 static int lp_tile_rows(int64_t rows, int64_t vocab) {
