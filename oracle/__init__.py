@@ -16,6 +16,8 @@ What is here:
 * :mod:`oracle.brute` -- the same definitions in exact rational arithmetic
   (``fractions``) with 60-digit ``decimal`` square roots, for tiny rows; it
   pins the float64 oracle.
+* :mod:`oracle.token_rows` -- embedding rows, RMS-normed rotated heads and log
+  probabilities in float64, with the magnitudes that error bounds multiply.
 * :mod:`oracle.check` -- the tolerance checks: the 1-bf16-ulp / 2e-6 relative
   contract, and the strict admissible-set check (float64 value at the bf16
   rounding points, widened by the spread an fp32 run may have; TensorFold PR

@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 OTHERS = ["ds_rows.o", "inst_l2.o", "inst_slerp.o", "inst_rownorm.o", "inst_l2_bwd.o",
           "inst_rownorm_bwd.o", "inst_act.o", "inst_qk.o", "inst_rescale.o", "inst_rms.o",
-          "inst_rms_bwd.o", "inst_colblock.o", "inst_embed.o", "inst_qk_rms.o", "inst_logprob.o"]
+          "inst_rms_bwd.o", "inst_colblock.o", "token_embed.o", "token_qk_rms.o", "token_logprob.o"]
 
 
 def asan_runtime():
