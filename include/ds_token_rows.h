@@ -84,7 +84,7 @@ int ds_embed_rows(const void* table, int32_t table_type, int64_t vocab, const vo
  * dtable   : [vocab, cols] of grad_type (fp32, or bf16 as
  *            ds_weight_rownorm_gain_backward takes its dw_eff), contiguous,
  *            16-byte aligned, overlapping no input.
- * rows     : 0 <= rows <= 2^30.
+ * rows     : 0 <= rows <= 2^30; dy and dtable hold at most 400 GiB each.
  */
 int ds_embed_rows_backward(const uint16_t* dy, const void* ids, int32_t id_bytes, float scale,
                            void* dtable, int32_t grad_type, int32_t accumulate, int64_t vocab,

@@ -19,6 +19,7 @@ using namespace dsh;
 
 constexpr int64_t kMostBytes = INT64_MAX / 8;
 constexpr int64_t kMostGradRows = 1 << 30;   // of an embedding's gradient
+constexpr int64_t kMostGradBytes = 400ll << 30;   // of its table and of its rows (a grid's limit)
 
 bool type_ok(int32_t t) { return t == DS_TYPE_BF16 || t == DS_TYPE_F32; }
 int64_t type_bytes(int32_t t) { return t == DS_TYPE_F32 ? 4 : 2; }
@@ -41,6 +42,11 @@ int check_embed(int32_t type, int64_t vocab, int32_t id_bytes, float scale, int6
   if (vocab < 0 || vocab > INT32_MAX || vocab > kMostBytes / (cols * 4)) return DS_ERR_SHAPE;
   if (!type_ok(type) || !id_bytes_ok(id_bytes) || !std::isfinite(scale)) return DS_ERR_ARG;
   return DS_OK;
+}
+
+bool grad_sizes_ok(int32_t type, int64_t vocab, int64_t rows, int64_t cols) {
+  return rows <= kMostGradRows && rows <= kMostGradBytes / (cols * 2) &&
+         vocab <= kMostGradBytes / (cols * type_bytes(type));
 }
 
 }  // namespace
@@ -79,7 +85,7 @@ int ds_embed_rows(const void* table, int32_t table_type, int64_t vocab, const vo
 int64_t ds_embed_rows_backward_workspace(int64_t vocab, int64_t rows, int64_t cols) {
   int st = check_embed(DS_TYPE_F32, vocab, 8, 1.f, rows, cols);
   if (st != DS_OK) return st;
-  if (rows > kMostGradRows) return DS_ERR_SHAPE;
+  if (!grad_sizes_ok(DS_TYPE_BF16, vocab, rows, cols)) return DS_ERR_SHAPE;
   return vocab == 0 ? 0 : dsr::embed_grad_workspace(vocab, rows, cols);
 }
 
@@ -89,7 +95,7 @@ int ds_embed_rows_backward(const uint16_t* dy, const void* ids, int32_t id_bytes
                            ds_stream_t stream) {
   int st = check_embed(grad_type, vocab, id_bytes, scale, rows, cols);
   if (st != DS_OK) return st;
-  if (rows > kMostGradRows) return DS_ERR_SHAPE;
+  if (!grad_sizes_ok(grad_type, vocab, rows, cols)) return DS_ERR_SHAPE;
   if (accumulate != 0 && accumulate != 1) return DS_ERR_ARG;
   if (vocab == 0 || (rows == 0 && accumulate)) return DS_OK;
   if (dtable == nullptr || (rows > 0 && (dy == nullptr || ids == nullptr))) return DS_ERR_NULL;

@@ -135,6 +135,23 @@ def test_gradient_of_whole_numbers_is_exact(B):
     assert np.array_equal(host(got), want)
 
 
+@pytest.mark.parametrize("vocab", [600_007, 2_097_153])
+def test_gradient_of_a_large_vocabulary(B, vocab):
+    """More tokens than 256 workgroups count at once."""
+    import torch
+    rng = np.random.default_rng(vocab)
+    rows = 5003
+    dy = rng.integers(-3, 4, (rows, 8)).astype(np.float32)       # whole numbers: exact sums
+    ids = rng.integers(0, vocab, rows)
+    ids[::7] = vocab - 1
+    ids[1::11] = 255
+    announce("embed gradient, vocabulary of", vocab)
+    got = host(grad(B, dy, dev(ids), vocab, 1.0))
+    want = np.zeros((vocab, 8), np.float32)
+    np.add.at(want, ids, dy)
+    assert np.array_equal(got, want)
+
+
 def test_gradient_of_no_rows_and_no_known_token(B):
     import torch
     announce("embed gradient of nothing")

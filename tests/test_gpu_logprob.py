@@ -96,6 +96,18 @@ def test_forward(B, rows, vocab, kind):
     check(c, c.forward(B, k), k)
 
 
+@pytest.mark.parametrize("rows,vocab,kind,values", [
+    (1, 1 << 20, "fp32", 0), (2, 300007, "bf16", 0), (3, 262145, "fp32", 5), (257, 20001, "bf16", 0)])
+def test_widest_rows(B, rows, vocab, kind, values):
+    """Rows over more waves than one wave joins lists of at a time; with few
+    distinct values the lists are all ties."""
+    c = Case(rows, vocab, kind, vocab, scaled=rows == 2)
+    if values:
+        c.x = np.random.default_rng(1).integers(0, values, c.x.shape).astype(np.float32)
+    announce("logprob", rows, vocab, kind)
+    check(c, c.forward(B, 32), 32)
+
+
 @pytest.mark.parametrize("top_k", [0, 1, 2, 5, 31, 32])
 @pytest.mark.parametrize("vocab", [32, 9000, 40001])
 def test_top_counts(B, top_k, vocab):
@@ -309,6 +321,32 @@ def test_gradient_in_place_and_masked(B):
     x = c.logits()
     got, ds2 = backward(B, c, r, logits=x, dlogits=x)
     assert got is x and torch.equal(bits(x), bits(want)) and torch.equal(bits(ds), bits(ds2))
+
+
+def test_gradient_of_a_large_batch(B):
+    """Past 256 MiB of logits in and out the loads change; the bits do not."""
+    import torch
+    rows, vocab = 2103, 32003
+    g = torch.Generator(device="cuda:0").manual_seed(18)
+    x = torch.randn(rows, vocab, device="cuda:0", generator=g).mul_(3).bfloat16()
+    labels = torch.randint(0, vocab, (rows,), device="cuda:0", generator=g)
+    scale = torch.rand(vocab, device="cuda:0", generator=g) + 0.5
+    dl, dh = torch.randn(2, rows, device="cuda:0", generator=g)
+    announce("logprob gradient, large", rows, vocab)
+    r = B.ds_logprob_rows(x, labels, scale)
+    whole, ds = B.ds_logprob_rows_backward(x, labels, r.lse, r.entropy, dl, dh, scale)
+    total = torch.zeros(vocab, dtype=torch.float64, device="cuda:0")
+    size = torch.zeros_like(total)
+    for i in range(0, rows, 300):
+        s = slice(i, i + 300)
+        part, dsp = B.ds_logprob_rows_backward(x[s], labels[s], r.lse[s], r.entropy[s], dl[s], dh[s], scale)
+        assert torch.equal(bits(whole[s]), bits(part)), i
+        total += dsp.double()
+        # what dscale sums, from the bf16 gradients: good enough for a magnitude
+        size += (part.double() / scale * x[s].double()).abs().sum(0)
+    torch.cuda.synchronize()
+    # two orders of the same fp32 sums over 2,103 rows
+    close(host(ds), host(total), 2 * rows * U * host(size) * 1.01, "dscale")
 
 
 def test_gradient_leaves_the_padding(B):

@@ -93,6 +93,8 @@ def test_valid_arguments_reach_the_device(L, call):
     (embed, dict(out=P[1]), B.DS_ERR_ARG),
     (embed_bwd, dict(dy=None), B.DS_ERR_NULL), (embed_bwd, dict(ids=None), B.DS_ERR_NULL),
     (embed_bwd, dict(dtable=None), B.DS_ERR_NULL), (embed_bwd, dict(rows=1 << 31), B.DS_ERR_SHAPE),
+    (embed_bwd, dict(rows=1 << 30, cols=1024), B.DS_ERR_SHAPE),       # 2 TiB of rows
+    (embed_bwd, dict(vocab=1 << 28, cols=1024), B.DS_ERR_SHAPE),      # 1 TiB of table
     (embed_bwd, dict(cols=12), B.DS_ERR_SHAPE), (embed_bwd, dict(accumulate=2), B.DS_ERR_ARG),
     (embed_bwd, dict(type=7), B.DS_ERR_ARG), (embed_bwd, dict(scale=-INF), B.DS_ERR_ARG),
     (embed_bwd, dict(dy=P[0] + 8), B.DS_ERR_ALIGN), (embed_bwd, dict(dtable=P[0]), B.DS_ERR_ARG),
