@@ -1,6 +1,9 @@
 /*
  * ds_rows.h -- row-wise L2 normalisation on AMD Instinct MI355X (gfx950).
  *
+ * (ds_token_rows.h declares the library's other entry points: embedding rows,
+ * RMS-normed q/k heads, log probabilities of logits.)
+ *
  * A C ABI over hand-written HIP kernels.  Plain pointers and sizes; no HIP or
  * torch types except an opaque stream handle.  All element buffers are device
  * memory unless stated otherwise.

@@ -57,6 +57,9 @@ def test_forward_of_nothing(B):
     y = B.ds_embed_rows(t, torch.zeros(3, dtype=torch.int64, device="cuda:0"))
     torch.cuda.synchronize()
     assert not y.float().any()
+    y = B.ds_embed_rows(torch.ones(4, 64, device="cuda:0"), torch.tensor([4, -1, 0], device="cuda:0"), -1.0)
+    torch.cuda.synchronize()
+    assert not bits(y[:2]).any() and (y[2] == -1).all()         # +0 under a negative scale
 
 
 def test_forward_table_past_4_gib(B):
