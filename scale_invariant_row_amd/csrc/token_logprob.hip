@@ -20,9 +20,9 @@
 //
 // Masked tokens (z = -inf) have exp 0 but 0 * -inf in T.  The fast sums go
 // without a test for them: a chunk whose sums come out NaN, or past 2^20, or
-// that holds nothing above -inf, is summed again in the careful form (lp_careful), where
-// the factor is clamped at -200 (exp is 0 there already); a NaN of the row's
-// own stays NaN.
+// that holds nothing above -inf, or lies millions from 0, is summed again in
+// the careful form (lp_careful), where the factor is clamped at -200 (exp is 0
+// there already); a NaN of the row's own stays NaN.
 #include <algorithm>
 #include <type_traits>
 
@@ -258,7 +258,9 @@ __device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float m) {
 // the careful form takes over.  With c = fp32(M log2 e) the sums
 // are about c in log2 units, z log2 e - c one fused multiply-add; r, the
 // rounding error of c (a fused multiply-add gives it exactly), turns them into
-// those about M:  z log2 e - c = (z - M) log2 e + r.
+// those about M:  z log2 e - c = (z - M) log2 e + r.  Beside a c past 2^24 r is
+// no longer a fraction (a chunk masked with -1e30 has one of 1e21, and S
+// would be 0 or infinite): the careful form again.
 __device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float m) {
   const float M = __builtin_bit_cast(
       float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, m)));
@@ -272,8 +274,8 @@ __device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float m)
   }
   S = wave_sum(S);
   T = wave_sum(T);
-  if (!(S < 0x1p20f && T == T)) return lp_careful(z, m);               // uniform
   const float r = __builtin_fmaf(M, kLog2e, -c);
+  if (!(S < 0x1p20f && T == T && fabsf(r) <= 0.5f)) return lp_careful(z, m);   // uniform
   const float f = __builtin_amdgcn_exp2f(-r);
   return LpSum{M, S * f, (T - r * S) * f * kLn2};
 }

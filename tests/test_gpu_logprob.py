@@ -182,6 +182,25 @@ def test_lowest_finite_masks_and_large_values(B):
     assert abs(host(r.entropy)[1] - np.log(9999)) < 1e-5
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [-1e9, -1e10, -1e30, -3e37, 1e8, 1e10, 1e12, 2e37, -7e14, 5e20])
+def test_finite_masks_of_any_size(B, kind, value):
+    """A finite mask over a whole chunk, over every token, and over all but a
+    few of one row: whichever way the value's product with log2 e rounds."""
+    c = Case(8, 4500, kind, 19, scaled=False)
+    rnd = bf16_round if kind == "bf16" else np.float32
+    c.x[0, 2048:4096] = rnd([value])[0]
+    c.x[1] = rnd([value])[0]
+    c.x[2, 5:] = rnd([value])[0]
+    for i in range(3, 8):                               # other values, other roundings
+        c.x[i] = rnd(np.array([value * (1 + 0.15 * i)], np.float32))[0]
+    c.labels[:] = 2100
+    announce("logprob finite masks", kind, value)
+    r = c.forward(B, 4)
+    check(c, r, 4)
+    assert (np.abs(host(r.entropy)[[1, 3, 4, 5, 6, 7]] - np.log(4500)) < 1e-5).all()
+
+
 def test_nonfinite(B):
     c = Case(5, 9000, "fp32", 7, scaled=False)
     c.x[0, 17] = np.nan
