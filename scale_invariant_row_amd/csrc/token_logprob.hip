@@ -570,8 +570,9 @@ hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace,
 // GPU); eight rows loaded together where the logits stream (844 us with four),
 // four where they come from the cache (15.5 against 16.8 us for 509 x 32,003).
 //
-// lp is clamped at -200, where p is 0, so that a masked token's 0 * inf does
-// not arise; c is NaN where lse is, so that row's NaN is kept.
+// lp is clamped at -200, where p is 0, and x at the largest finite value, so
+// that a masked token's 0 * inf does not arise; c is NaN where lse is, so that
+// row's NaN is kept.
 
 struct LpRowGrad {
   float lse, gh, c, hot;       // hot: tau dlogp, added at the label
@@ -690,14 +691,19 @@ logprob_grad_kernel(const LogprobGradArgs a, int strips, int tile_rows, float* p
       }
       if (r.label >= c0 && r.label < c0 + 256 * VE) {               // uniform
 #pragma unroll
-        for (int k = 0; k < VE; ++k)
-          if (c + k == r.label && L::get(t[i], k) > -__builtin_inff()) d[k] += r.hot;
+        for (int k = 0; k < VE; ++k) {
+          float z = L::get(t[i], k);
+          if constexpr (SCALED) z = z * sc[k];
+          if (c + k == r.label && z * a.inv_temp > -__builtin_inff()) d[k] += r.hot;
+        }
       }
       if constexpr (SCALED) {
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
           if (parts != nullptr)
-            sum[k] = __builtin_fmaf(d[k], fmaxf(L::get(t[i], k), -0x1.fffffep127f), sum[k]);
+            sum[k] = __builtin_fmaf(
+                d[k], __builtin_amdgcn_fmed3f(L::get(t[i], k), -0x1.fffffep127f, 0x1.fffffep127f),
+                sum[k]);
           d[k] = d[k] * sc[k];
         }
       }

@@ -342,6 +342,25 @@ def test_gradient_in_place_and_masked(B):
     assert got is x and torch.equal(bits(x), bits(want)) and torch.equal(bits(ds), bits(ds2))
 
 
+def test_gradient_of_tokens_masked_by_their_scale(B):
+    """z is -infinity although x is not: a product past fp32's range, and
+    +infinity under a negative scale.  No gradient, as a label too."""
+    c = Case(12, 3001, "fp32", 20)
+    c.scale[40], c.scale[2500] = -2.0, -1.5
+    c.x[0, 40] = 3e38
+    c.x[4, 2500] = np.inf
+    c.x[5, 2500] = np.inf
+    c.labels[[0, 4, 5]] = 40, 2500, 7
+    announce("logprob gradient, masked by the scale")
+    with np.errstate(over="ignore"):
+        r = c.forward(B, 3)
+        check(c, r, 3)
+        d, ds = backward(B, c, r)
+        c.x[[4, 5], 2500] = np.where(np.isinf(c.x[[4, 5], 2500]), np.float32(3e38), 0)   # z is the same
+        check_backward(c, r, d, ds)
+    assert host(d)[0, 40] == 0 and not host(d)[[4, 5], 2500].any()
+
+
 def test_gradient_of_a_large_batch(B):
     """Past 256 MiB of logits in and out the loads change; the bits do not."""
     import torch
