@@ -213,6 +213,10 @@ int64_t ds_logprob_rows_workspace(int64_t rows, int64_t vocab, int32_t top_k);
  * dscale   : [vocab] fp32, needs scale; or NULL when not wanted.  rows == 0
  *            writes zeros.
  * A masked token gets no gradient, and a row with every token masked none.
+ * p_j is exp(z_j - lse) of the lse given, so it is known to |lse| 2^-24 of
+ * itself: fp32 logits thousands from zero lose digits of their gradient, and
+ * a row with |lse| >= 2^24 (a finite mask, as -1e30, over every token) counts
+ * as masked whole and gets none.
  */
 int ds_logprob_rows_backward(const void* logits, int32_t logits_type, int64_t ld,
                              const float* scale, float inv_temp, const void* labels,

@@ -589,7 +589,10 @@ __device__ __forceinline__ LpRowGrad lp_row_grad(const LogprobGradArgs& a, int64
   r.c = a.dentropy != nullptr ? -__builtin_fmaf(h, a.entropy[row], g) : -g;
   r.hot = g;
   if (r.lse != r.lse) r.c = r.lse;
-  if (r.lse == -__builtin_inff()) {                   // every token masked: no gradient
+  // every token masked, or all so far from 0 (a finite mask over the row) that
+  // fp32 holds the maximum alone and not the log of the sum beside it, which
+  // would make p 1 for each of them: no gradient
+  if (fabsf(r.lse) >= 0x1p24f) {
     r.lse = __builtin_inff();
     r.hot = 0.f;
   }

@@ -361,6 +361,27 @@ def test_gradient_of_tokens_masked_by_their_scale(B):
     assert host(d)[0, 40] == 0 and not host(d)[[4, 5], 2500].any()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [-3.3e38, -1e30, -1e9, 1e12])
+def test_gradient_of_rows_masked_with_finite_values(B, kind, value):
+    """Such a row gets no gradient and adds none to dscale; a finite mask over
+    part of a row is like any logit."""
+    c = Case(10, 2500, kind, 21, inv_temp=0.9)
+    c.scale[:] = 1
+    c.x[2] = value
+    c.x[5, :2100] = -abs(value)
+    c.labels[2], c.labels[5] = 9, 2400
+    if kind == "bf16":
+        c.x = bf16_round(c.x)
+    announce("logprob gradient, finite masks", kind, value)
+    r = c.forward(B, 3)
+    check(c, r, 3)
+    d, ds = backward(B, c, r)
+    assert not host(d)[2].any()
+    c.x[2] = -np.inf                                    # what the row counts as
+    check_backward(c, r, d, ds)
+
+
 def test_gradient_of_a_large_batch(B):
     """Past 256 MiB of logits in and out the loads change; the bits do not."""
     import torch
