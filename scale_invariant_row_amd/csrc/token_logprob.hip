@@ -19,9 +19,9 @@
 // best of each row.
 //
 // Masked tokens (z = -inf) have exp 0 but 0 * -inf in T.  The fast sums go
-// without a test for them: a chunk whose sums come out NaN, or past 2^20, or
-// that holds nothing above -inf, or lies millions from 0, is summed again in
-// the careful form (lp_careful), where the factor is clamped at -200 (exp is 0
+// without a test for them: a chunk whose T comes out NaN (a masked token in it,
+// or nothing above -inf) or that lies millions from 0 is summed again in the
+// careful form (lp_careful), where the factor is clamped at -200 (exp is 0
 // there already); a NaN of the row's own stays NaN.
 #include <algorithm>
 #include <type_traits>
@@ -237,10 +237,31 @@ __device__ __forceinline__ void lp_load_scale(float (&sc)[kLpPer], const float* 
   }
 }
 
-// S and T about the chunk's maximum with every step guarded: see the head of
-// this file.  m: the lane's maximum.
-__device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float m) {
-  const float M = wave_max(m);
+// The wave's maximum of a value that is no NaN, in every lane.  Ordered as whole
+// numbers, so that each step is one instruction (fmaxf would quiet NaNs of both
+// sides first): within 16 lanes, then row after row into the last lane.
+template <int CTRL>
+__device__ __forceinline__ int lp_max_step(int v) {
+  const int o = __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
+  return v > o ? v : o;
+}
+
+__device__ __forceinline__ float lp_wave_max(float m) {
+  const int u = __builtin_bit_cast(int, m);
+  int v = u ^ ((u >> 31) & 0x7fffffff);
+  v = lp_max_step<0xB1>(v);    // quad_perm [1,0,3,2]
+  v = lp_max_step<0x4E>(v);    // quad_perm [2,3,0,1]
+  v = lp_max_step<0x141>(v);   // row_half_mirror
+  v = lp_max_step<0x140>(v);   // row_mirror
+  v = lp_max_step<0x142>(v);   // row_bcast:15 (the first row gets 0: not lane 63's)
+  v = lp_max_step<0x143>(v);   // row_bcast:31
+  v = __builtin_amdgcn_readlane(v, 63);
+  return __builtin_bit_cast(float, v ^ ((v >> 31) & 0x7fffffff));
+}
+
+// S and T about the chunk's maximum M with every step guarded: see the head of
+// this file.
+__device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float M) {
   const float base = M == -__builtin_inff() ? 0.f : M;
   float S = 0.f, T = 0.f;
 #pragma unroll
@@ -252,18 +273,18 @@ __device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float m) {
   return LpSum{M, wave_sum(S), wave_sum(T)};
 }
 
-// A chunk's sums, the same in every lane.  Any base near the maximum will do,
-// and lane 0's maximum needs no exchange; where the chunk reaches so far above
-// it that S passes 2^20 (and log S and T / S would lose digits to each other),
-// the careful form takes over.  With c = fp32(M log2 e) the sums
-// are about c in log2 units, z log2 e - c one fused multiply-add; r, the
-// rounding error of c (a fused multiply-add gives it exactly), turns them into
-// those about M:  z log2 e - c = (z - M) log2 e + r.  Beside a c past 2^24 r is
-// no longer a fraction (a chunk masked with -1e30 has one of 1e21, and S
-// would be 0 or infinite): the careful form again.
+// A chunk's sums, the same in every lane; m: the lane's maximum.  They are
+// about the chunk's own maximum M: the top's term is 1, S >= 1, and neither
+// log S nor T / S is larger than it has to be.  (A base that needs no exchange
+// between lanes, such as lane 0's maximum, lets both grow to some 13 in rows
+// whose top stands out, and they lose that many digits to each other.)  With
+// c = fp32(M log2 e) the sums are about c in log2 units, z log2 e - c one fused
+// multiply-add; r, the rounding error of c (a fused multiply-add gives it
+// exactly), turns them into those about M:  z log2 e - c = (z - M) log2 e + r.
+// Beside a c past 2^24 r is no longer a fraction (a chunk masked with -1e30 has
+// one of 1e21, and S would be 0 or infinite): the careful form then.
 __device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float m) {
-  const float M = __builtin_bit_cast(
-      float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, m)));
+  const float M = lp_wave_max(m);
   const float c = M * kLog2e;
   float S = 0.f, T = 0.f;
 #pragma unroll
@@ -275,7 +296,7 @@ __device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float m)
   S = wave_sum(S);
   T = wave_sum(T);
   const float r = __builtin_fmaf(M, kLog2e, -c);
-  if (!(S < 0x1p20f && T == T && fabsf(r) <= 0.5f)) return lp_careful(z, m);   // uniform
+  if (!(T == T && fabsf(r) <= 0.5f)) return lp_careful(z, M);   // uniform
   const float f = __builtin_amdgcn_exp2f(-r);
   return LpSum{M, S * f, (T - r * S) * f * kLn2};
 }

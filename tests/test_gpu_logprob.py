@@ -484,3 +484,48 @@ def test_no_rows(B):
     d, ds = backward(B, c, r)
     assert r.logp.shape == (0,) and r.top_ids.shape == (0, 3) and d.shape == (0, 100)
     assert not ds.any()
+
+
+@pytest.mark.parametrize("rows,vocab,kind", [(300, 2048, "fp32"), (300, 2048, "bf16"), (200, 5000, "fp32"),
+                                             (200, 9000, "bf16"), (4099, 2100, "fp32"), (4098, 4096, "bf16"),
+                                             (12, 131072, "fp32")])
+def test_confident_rows(B, rows, vocab, kind):
+    """One token 2 to 14 above all others, as in a trained model, in another
+    lane than the first.
+
+    With m = z_top and s the sum of the others' exp(z - m), S = 1 + s.  The top
+    is its lane's last value of the chunk, so what rounds a sum of 1 or more is
+    its own exponential (2 u), 6 sums over the lanes, the chunk's correction
+    (6 u) and one addition in each of the 6 joins: 20 u, and 24 u with the
+    logarithm and its subtraction.  Every other term, s in all, is off by its
+    exponential's (2 + 2 |d|) u and by 70 u of sums at most."""
+    rng = np.random.default_rng(rows + vocab)
+    c = Case(rows, vocab, kind, vocab + 1, scaled=rows > 4000)
+    c.x[:] = rng.standard_normal(c.x.shape) * 0.5 - 3
+    if c.scale is not None:
+        c.scale = np.exp2(rng.integers(0, 2, vocab)).astype(np.float32)
+    # the last of the 32 values of lane 20, in a whole chunk
+    top = (vocab // 2048 - 1) * 2048 + ((3 * 64 + 20) * 8 + 7 if kind == "bf16" else (7 * 64 + 20) * 4 + 3)
+    if c.scale is not None:
+        c.scale[top] = 1
+    c.x[:, top] = rng.uniform(0.5, 12.5, rows)
+    if kind == "bf16":
+        c.x = bf16_round(c.x)
+    c.labels[::2] = top
+    announce("logprob confident rows", rows, vocab, kind)
+    r = c.forward(B, 3)
+    check(c, r, 3)
+    z = c.z.astype(np.float64)
+    logp, ent, lse, ids, top_lp = T.logprob_rows(c.z, c.labels, 3)
+    d = z - z[:, top:top + 1]
+    assert (np.delete(d, top, 1) < 0).all()
+    e = np.exp(d)
+    e[:, top] = 0
+    s, s1, s2 = e.sum(-1), (e * -d).sum(-1), (e * d * d).sum(-1)
+    off = U * (24 + 72 * s + 2 * s1)                    # of log S
+    known = (c.labels >= 0) & (c.labels < vocab)
+    dy = np.where(known, np.abs(d[np.arange(rows), np.where(known, c.labels, 0)]), 0)
+    close(host(r.logp), logp, off + U * (dy + np.abs(logp)), "logp")
+    close(host(r.lse), lse, off + U * np.abs(lse), "lse")
+    close(host(r.top_logp), top_lp, off[:, None] + 2 * U * np.abs(top_lp), "top_logp")
+    close(host(r.entropy), ent, off + U * (3 * ent + 74 * s1 + 2 * s2), "entropy")
