@@ -205,7 +205,8 @@ int64_t ds_logprob_rows_workspace(int64_t rows, int64_t vocab, int32_t top_k);
  *   dscale_j  = sum over rows of dz_j inv_temp x_j          fp32
  *
  * lse, entropy : the forward call's outputs; entropy may be NULL when
- *            dentropy is.
+ *            dentropy is (rows with |lse| >= 2^24 then get no gradient, see
+ *            below).
  * dlogp, dentropy : [rows] fp32, the gradients reaching logp and entropy;
  *            either may be NULL (zero).  An ignored row's dlogp counts as 0.
  * dlogits  : [rows, ld_out], may be logits itself (with ld_out == ld);
@@ -214,9 +215,13 @@ int64_t ds_logprob_rows_workspace(int64_t rows, int64_t vocab, int32_t top_k);
  *            writes zeros.
  * A masked token gets no gradient, and a row with every token masked none.
  * p_j is exp(z_j - lse) of the lse given, so it is known to |lse| 2^-24 of
- * itself: fp32 logits thousands from zero lose digits of their gradient, and
- * a row with |lse| >= 2^24 (a finite mask, as -1e30, over every token) counts
- * as masked whole and gets none.
+ * itself: fp32 logits thousands from zero lose digits of their gradient.  From
+ * |lse| = 2^24 on lse holds the row's maximum alone, and the row has a gradient
+ * only where one token holds that maximum alone (a runaway logit, a temperature
+ * near 0), which the entropy tells: where it is given and below 0.6875 (n equal
+ * tokens have log n, 0.693 at least).  Any other such row (a finite mask, as
+ * -1e30, over every token; a maximum that tokens share) counts as masked whole
+ * and gets none.
  */
 int ds_logprob_rows_backward(const void* logits, int32_t logits_type, int64_t ld,
                              const float* scale, float inv_temp, const void* labels,

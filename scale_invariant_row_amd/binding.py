@@ -1009,7 +1009,9 @@ def ds_logprob_rows_backward(logits, labels, lse, entropy, dlogp, dentropy=None,
     """The gradient of ds_logprob_rows' logp and entropy: (dlogits, dscale).
 
     ``lse`` and ``entropy`` are the forward call's (entropy may be None
-    without ``dentropy``); ``dlogp``/``dentropy``: fp32 [rows] or None.
+    without ``dentropy``; a row with ``|lse| >= 2**24`` then gets no gradient,
+    and with it only if one token holds its maximum alone);
+    ``dlogp``/``dentropy``: fp32 [rows] or None.
     ``dlogits`` (like logits; may be logits itself) is allocated contiguous
     when not given; dscale is None without ``scale`` or ``want_dscale``.
     """

@@ -610,10 +610,13 @@ __device__ __forceinline__ LpRowGrad lp_row_grad(const LogprobGradArgs& a, int64
   r.c = a.dentropy != nullptr ? -__builtin_fmaf(h, a.entropy[row], g) : -g;
   r.hot = g;
   if (r.lse != r.lse) r.c = r.lse;
-  // every token masked, or all so far from 0 (a finite mask over the row) that
-  // fp32 holds the maximum alone and not the log of the sum beside it, which
-  // would make p 1 for each of them: no gradient
-  if (fabsf(r.lse) >= 0x1p24f) {
+  // Past 2^24 fp32 holds the row's maximum, but no log of the sum beside it: p
+  // comes out 1 for every token at the maximum.  That is right where one token
+  // holds it alone.  An entropy below log 2 = 0.693 says so: n tokens that share
+  // the maximum have log n at least.  Any other row (a finite mask over every
+  // token; and every token masked, lse -inf) has no gradient.
+  if (fabsf(r.lse) >= 0x1p24f &&
+      !(a.entropy != nullptr && a.entropy[row] < 0.6875f && fabsf(r.lse) < __builtin_inff())) {
     r.lse = __builtin_inff();
     r.hot = 0.f;
   }

@@ -529,3 +529,72 @@ def test_confident_rows(B, rows, vocab, kind):
     close(host(r.lse), lse, off + U * np.abs(lse), "lse")
     close(host(r.top_logp), top_lp, off[:, None] + 2 * U * np.abs(top_lp), "top_logp")
     close(host(r.entropy), ent, off + U * (3 * ent + 74 * s1 + 2 * s2), "entropy")
+
+
+@pytest.mark.parametrize("kind,scaled", [("fp32", False), ("fp32", True), ("bf16", False), ("bf16", True)])
+def test_gradient_of_one_token_far_from_the_others(B, kind, scaled):
+    """Past |lse| = 2^24 one token may still hold the maximum alone (a runaway
+    logit, a temperature near 0): its p is 1 and the row's gradient that of any
+    row, where the forward call's entropy tells so.  A maximum that tokens share
+    leaves p unknown: none, and none without the entropy either."""
+    import torch
+    c = Case(14, 4500, kind, 23, scaled=scaled, inv_temp=0.75)
+    rnd = bf16_round if kind == "bf16" else np.float32
+    if scaled:
+        c.scale[:] = np.exp2(np.random.default_rng(3).integers(-1, 2, 4500)).astype(np.float32)
+    top, alone, shared = 3001, [0, 1, 2, 3, 4, 5, 12], [6, 7, 8, 13]
+    c.x[0, top] = 4e8
+    c.x[1, top] = 2e30
+    c.x[2] = rnd([-3e30])[0] * (1 + np.arange(4500) % 7)    # far below, but for one
+    c.x[2, top] = rnd([-2e8])[0]
+    c.x[3] *= 1e9                                       # a temperature near 0
+    c.x[3, top] = 2e11
+    c.x[4, top] = 3e8                                   # its label the top, below a lesser one, ...
+    c.x[5] = -np.inf                                    # ... the only token that is not masked
+    c.x[5, top] = -4e8
+    c.x[12, top] = 4e8
+    c.labels[[0, 2, 3, 4, 5, 12]] = top, 17, top, top, 9, -7
+    c.labels[1] = 4499
+    c.x[6, [5, top]] = 1e10 / (1 if c.scale is None else c.scale[[5, top]])     # two hold the maximum
+    c.x[7] = -1e30 / (1 if c.scale is None else c.scale)                        # all do
+    c.x[8, :] = -np.inf
+    c.x[8, :3] = -1e9 / (1 if c.scale is None else c.scale[:3])
+    c.x[13, :] = 5e8 / (1 if c.scale is None else c.scale)
+    c.labels[shared] = 5, 9, 2, 3
+    c.x = rnd(c.x)
+    announce("logprob gradient of far rows", kind, scaled)
+    r = c.forward(B, 3)
+    check(c, r, 3)
+    lse, ent = host(r.lse), host(r.entropy)
+    assert (np.abs(lse[alone + shared]) >= 2.0 ** 24).all()
+    assert (np.abs(ent[alone]) < 1e-6).all() and (ent[shared] > 0.69).all()
+    d, ds = backward(B, c, r)
+    assert not host(d)[shared].any() and host(d)[5, 9] == 0
+    for i in (1, 2):                                    # the label's gradient and the top's
+        assert host(d)[i, c.labels[i]] != 0 and host(d)[i, top] != 0
+    # without the entropy no far row can tell
+    blind, _ = B.ds_logprob_rows_backward(c.logits(), dev(c.labels), r.lse, None, dev(c.g), None,
+                                          None if c.scale is None else dev(c.scale), 0.75)
+    torch.cuda.synchronize()
+    assert not host(blind)[alone + shared].any()
+    c.x[shared] = -np.inf                               # what they count as
+    check_backward(c, r, d, ds)
+
+
+def test_gradient_of_far_rows_with_a_second_token_near(B):
+    """Two tokens a few steps of fp32 apart past 2^24: lse is rounded by up to
+    2^-24 of itself (1.2 here), and p known to that."""
+    c = Case(2, 300, "fp32", 24, scaled=False)
+    c.x[:] = np.array([[2e7], [-2e7]], np.float32) - 400
+    c.x[0, [7, 250]] = 2e7, 2e7 - 4
+    c.x[1, [250, 7]] = -2e7, -2e7 - 6
+    c.labels[:] = 7
+    announce("logprob gradient of near tokens far from 0")
+    r = c.forward(B)
+    d, _ = backward(B, c, r, gh=False)
+    z = c.x.astype(np.float64)
+    p = np.exp(z - z.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    want = c.g[:, None] * ((np.arange(300) == 7) - p)
+    close(host(d), want, np.abs(c.g[:, None]) * p * np.expm1(2e7 * U) + 4 * U, "dlogits")
+    assert host(d)[0, 250] != 0 and host(d)[1, 7] != 0
