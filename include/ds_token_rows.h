@@ -213,7 +213,8 @@ int64_t ds_logprob_rows_workspace(int64_t rows, int64_t vocab, int32_t top_k);
  *            otherwise overlapping no input.
  * dscale   : [vocab] fp32, needs scale; or NULL when not wanted.  rows == 0
  *            writes zeros.
- * A masked token gets no gradient, and a row with every token masked none.
+ * A masked token (by its scale too: an infinite one, a product past fp32) gets
+ * no gradient, and a row with every token masked none.
  * p_j is exp(z_j - lse) of the lse given, so it is known to |lse| 2^-24 of
  * itself: fp32 logits thousands from zero lose digits of their gradient.  From
  * |lse| = 2^24 on lse holds the row's maximum alone, and the row has a gradient

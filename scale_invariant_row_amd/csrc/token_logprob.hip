@@ -591,9 +591,14 @@ hipError_t launch_logprob_rows(bool f32, const LogprobArgs& a, void* workspace,
 // GPU); eight rows loaded together where the logits stream (844 us with four),
 // four where they come from the cache (15.5 against 16.8 us for 509 x 32,003).
 //
-// lp is clamped at -200, where p is 0, and x at the largest finite value, so
-// that a masked token's 0 * inf does not arise; c is NaN where lse is, so that
-// row's NaN is kept.
+// lp is clamped at -200, where p is 0, and x and the scale at the largest
+// finite value where d multiplies them, so that a masked token's 0 * inf does
+// not arise; c is NaN where lse is, so that row's NaN is kept.
+
+// An infinity as the largest finite value of its sign.
+__device__ __forceinline__ float lp_finite(float v) {
+  return __builtin_amdgcn_fmed3f(v, -0x1.fffffep127f, 0x1.fffffep127f);
+}
 
 struct LpRowGrad {
   float lse, gh, c, hot;       // hot: tau dlogp, added at the label
@@ -728,10 +733,8 @@ logprob_grad_kernel(const LogprobGradArgs a, int strips, int tile_rows, float* p
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
           if (parts != nullptr)
-            sum[k] = __builtin_fmaf(
-                d[k], __builtin_amdgcn_fmed3f(L::get(t[i], k), -0x1.fffffep127f, 0x1.fffffep127f),
-                sum[k]);
-          d[k] = d[k] * sc[k];
+            sum[k] = __builtin_fmaf(d[k], lp_finite(L::get(t[i], k)), sum[k]);
+          d[k] = d[k] * lp_finite(sc[k]);
         }
       }
       L::store(a.dx, (row0 + r0 + i) * a.ldo, c, a.vocab, L::put(d));

@@ -598,3 +598,25 @@ def test_gradient_of_far_rows_with_a_second_token_near(B):
     want = c.g[:, None] * ((np.arange(300) == 7) - p)
     close(host(d), want, np.abs(c.g[:, None]) * p * np.expm1(2e7 * U) + 4 * U, "dlogits")
     assert host(d)[0, 250] != 0 and host(d)[1, 7] != 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_gradient_of_tokens_masked_by_an_infinite_scale(B, kind):
+    """A scale of -infinity or +infinity with logits of the other sign masks a
+    column: no gradient for its logits or its scale."""
+    c = Case(40, 3001, kind, 25, inv_temp=1.2)
+    c.scale[[3, 1500, 3000]] = np.inf, -np.inf, np.inf
+    c.x[:, [3, 3000]] = -np.abs(c.x[:, [3, 3000]]) - 0.1
+    c.x[:, 1500] = np.abs(c.x[:, 1500]) + 0.1
+    if kind == "bf16":
+        c.x = bf16_round(c.x)
+    c.labels[[4, 9]] = 3, 1500
+    announce("logprob gradient, infinite scale", kind)
+    r = c.forward(B, 3)
+    check(c, r, 3)
+    d, ds = backward(B, c, r)
+    for a in (host(d)[:, [3, 1500, 3000]], host(ds)[[3, 1500, 3000]]):
+        assert not a.any() and not np.isnan(a).any()
+    # a masked column by another way: the rest must not tell the difference
+    c.x[:, [3, 1500, 3000]], c.scale[[3, 1500, 3000]] = -np.inf, 1
+    check_backward(c, r, d, ds)
