@@ -202,7 +202,8 @@ int64_t ds_logprob_rows_workspace(int64_t rows, int64_t vocab, int32_t top_k);
  *
  *   dz_j      = dlogp ([j = label] - p_j) - dentropy p_j (z_j - lse + entropy)
  *   dlogits_j = dz_j inv_temp scale_j            in logits_type
- *   dscale_j  = sum over rows of dz_j inv_temp x_j          fp32
+ *   dscale_j  = sum over rows of dz_j inv_temp x_j          fp32: up to 32 rows
+ *               in fp32, these sums in fp64
  *
  * lse, entropy : the forward call's outputs; entropy may be NULL when
  *            dentropy is (rows with |lse| >= 2^24 then get no gradient, see

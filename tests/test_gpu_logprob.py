@@ -620,3 +620,36 @@ def test_gradient_of_tokens_masked_by_an_infinite_scale(B, kind):
     # a masked column by another way: the rest must not tell the difference
     c.x[:, [3, 1500, 3000]], c.scale[[3, 1500, 3000]] = -np.inf, 1
     check_backward(c, r, d, ds)
+
+
+@pytest.mark.parametrize("rows", [300000, 1 << 20])
+def test_column_sums_of_many_tiles(B, rows):
+    """One row's share of dscale is near 2^30, the others' near 1: thousands of tiles
+    of at most 32 rows.  A tile's sum rounds 32 times; adding the tiles and
+    rounding the total adds 2 more, however many there are."""
+    import torch
+    announce("logprob column sums over", rows)
+    g = torch.Generator(device="cuda:0").manual_seed(26)
+    x = torch.randn(rows, 6, device="cuda:0", generator=g)
+    labels = torch.randint(0, 6, (rows,), device="cuda:0", generator=g)
+    scale = torch.rand(6, device="cuda:0", generator=g) + 0.5
+    dl = torch.rand(rows, device="cuda:0", generator=g) + 0.5
+    dl[0] = 2.0 ** 31
+    # labels of one half of the tokens and x < 0 in the other: one sign there
+    labels %= 3
+    labels[0] = 0
+    x[:, 3:].abs_().neg_()
+    x[0] = -1
+    r = B.ds_logprob_rows(x, labels, scale)
+    d, ds = B.ds_logprob_rows_backward(x, labels, r.lse, None, dl, None, scale)
+    torch.cuda.synchronize()
+    z = (x * scale).double()
+    lp = z - r.lse.double()[:, None]
+    p = torch.exp(lp)
+    hot = torch.zeros_like(p).scatter_(1, labels[:, None], 1.0)
+    t = dl.double()[:, None] * (hot - p) * x.double()
+    unit = dl.double()[:, None] * (p * (lp.abs() + 1) + hot) * x.double().abs()
+    bound = 10 * U * unit.sum(0) + 34 * U * t.abs().sum(0)
+    lost = t[32:].abs().sum(0)                          # what a sum that sticks at the first would miss
+    assert (lost[3:] > 2 * bound[3:]).all()
+    close(host(ds), host(t.sum(0)), host(bound), "dscale")
