@@ -653,3 +653,51 @@ def test_column_sums_of_many_tiles(B, rows):
     lost = t[32:].abs().sum(0)                          # what a sum that sticks at the first would miss
     assert (lost[3:] > 2 * bound[3:]).all()
     close(host(ds), host(t.sum(0)), host(bound), "dscale")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_more_rows_than_one_launch(B, kind):
+    """The forward call launches 2^20 rows at a time."""
+    import torch
+    rows, vocab, at = (1 << 20) + 37, 11, [0, 5, (1 << 20) - 3, 1 << 20]
+    announce("logprob, two launches", kind)
+    g = torch.Generator(device="cuda:0").manual_seed(27)
+    x = torch.randn(rows, vocab, device="cuda:0", generator=g).mul_(2)
+    x = x.bfloat16() if kind == "bf16" else x
+    labels = torch.randint(-1, vocab, (rows,), device="cuda:0", generator=g)
+    for ids, scale in ((labels, None), (labels.int(), torch.rand(vocab, device="cuda:0", generator=g) + 0.5)):
+        whole = B.ds_logprob_rows(x, ids, scale, 0.9, 4)
+        for i in at:
+            n = min(40, rows - i)
+            part = B.ds_logprob_rows(x[i:i + n], ids[i:i + n], scale, 0.9, 4)
+            torch.cuda.synchronize()
+            for a, b in zip(whole, part):
+                assert torch.equal(bits(a[i:i + n]), bits(b)), i
+        z = (x.float() if scale is None else x.float() * scale) * 0.9
+        lse = torch.logsumexp(z.double(), -1)
+        assert float((whole.lse.double() - lse).abs().max()) < 256 * U * 16
+
+
+def test_gradient_of_more_tiles_than_one_launch(B):
+    """The gradient launches 2^20 tiles' strips at a time: 32 rows each here."""
+    import torch
+    rows, vocab = (1 << 25) + 32 * 3 + 5, 3
+    announce("logprob gradient, two launches")
+    g = torch.Generator(device="cuda:0").manual_seed(28)
+    x = torch.randn(rows, vocab, device="cuda:0", generator=g).bfloat16()
+    labels = torch.randint(0, vocab, (rows,), device="cuda:0", generator=g, dtype=torch.int32)
+    scale = torch.rand(vocab, device="cuda:0", generator=g) + 0.5
+    dl, dh = torch.rand(2, rows, device="cuda:0", generator=g) + 0.5
+    r = B.ds_logprob_rows(x, labels, scale)
+    d, ds = B.ds_logprob_rows_backward(x, labels, r.lse, r.entropy, dl, dh, scale)
+    total = torch.zeros(vocab, dtype=torch.float64, device="cuda:0")
+    size = torch.zeros_like(total)
+    for i, n in ((0, 1 << 24), (1 << 24, (1 << 24) - 7), ((1 << 25) - 7, rows - (1 << 25) + 7)):
+        s = slice(i, i + n)
+        part, dsp = B.ds_logprob_rows_backward(x[s], labels[s], r.lse[s], r.entropy[s], dl[s], dh[s], scale)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(d[s]), bits(part)), i
+        total += dsp.double()
+        size += (part.float() / scale * x[s].float()).abs().sum(0, dtype=torch.float64)
+    # two groupings of the same fp32 terms: 32 roundings a tile and 2 of the totals each
+    close(host(ds), host(total), 2 * 34 * U * host(size) * 1.01, "dscale")
