@@ -16,7 +16,7 @@
  *
  * Numerics.  bf16 values are passed as their 16-bit patterns.  Everything is
  * computed in fp32 (a rotation's angle in fp64) and rounded once, to nearest
- * even, into each bf16 output.  Sums are held in fp32.
+ * even, into each bf16 output.  Sums are held in fp32 or more.
  *
  * Determinism.  The bits of an output row depend on that row's inputs and the
  * row width alone, not on the row count, the grid or the stream.  A gradient

@@ -72,7 +72,7 @@ hipError_t launch_embed_rows(bool f32, bool wide_ids, const EmbedArgs& a, int gr
 // (embed_sum_kernel), and join the sums of tokens that span blocks
 // (embed_join_kernel).  A token's rows are added in ascending order within a
 // block and its blocks in order, so the ids fix the order of every sum, and no
-// token, however often it occurs, holds one wave up for all its rows.
+// wave takes all rows of a token that occurs often, only its blocks' sums.
 //
 // Tokens are dealt over `parts` groups, a power of two: token t is number
 // t / parts of group t mod parts, so that the frequent low ids of a frequency-
@@ -427,7 +427,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const EmbedGradArgs a, c
 }
 
 // Tokens that span blocks: the wave of the block that a token starts in adds
-// part 1 of it and part 0 of the blocks that follow, in order.
+// part 1 of it and part 0 of the blocks that follow, in order.  11 us where the
+// most frequent of 32,768 tokens fills some 60 blocks.  A token that fills the
+// whole batch is bound by this one wave for each 64 VE columns: 1,023 parts of
+// 4,096 columns take 91 us into an fp32 row, 251 into a bf16 one (half the
+// waves), beside 119 of sorting (one workgroup places every row) and 45 to 49
+// of sums.
 template <bool F32, bool ACC>
 __global__ void __launch_bounds__(256)
 embed_join_kernel(const EmbedGradArgs a, const EmbedSort w, int tiles) {

@@ -15,14 +15,16 @@
 // Cost per value beside its load: unpack, scale, half a maximum, one fused
 // multiply-add to log2 units, exp2 (four issue slots), a sum and a fused
 // multiply-add: 10 slots, 270 us for 8,192 x 131,072 bf16 values, under the
-// time their 2.1 GB take from memory.  Measured: 402 us (5.3 TB/s) with the 5
-// best of each row.
+// time their 2.1 GB take from memory.  Measured: 409 us (5.3 TB/s) with the 5
+// best of each row, 363 without.
 //
 // Masked tokens (z = -inf) have exp 0 but 0 * -inf in T.  The fast sums go
 // without a test for them: a chunk whose T comes out NaN (a masked token in it,
 // or nothing above -inf) or that lies millions from 0 is summed again in the
 // careful form (lp_careful), where the factor is clamped at -200 (exp is 0
-// there already); a NaN of the row's own stays NaN.
+// there already); a NaN of the row's own stays NaN.  With a token masked in
+// every chunk that is every chunk twice: 8,192 x 131,072 with 30 % of the
+// columns at -inf takes 565 us, with -1e30 there 409.
 #include <algorithm>
 #include <type_traits>
 
@@ -275,14 +277,16 @@ __device__ __forceinline__ LpSum lp_careful(const float (&z)[kLpPer], float M) {
 
 // A chunk's sums, the same in every lane; m: the lane's maximum.  They are
 // about the chunk's own maximum M: the top's term is 1, S >= 1, and neither
-// log S nor T / S is larger than it has to be.  (A base that needs no exchange
-// between lanes, such as lane 0's maximum, lets both grow to some 13 in rows
-// whose top stands out, and they lose that many digits to each other.)  With
-// c = fp32(M log2 e) the sums are about c in log2 units, z log2 e - c one fused
-// multiply-add; r, the rounding error of c (a fused multiply-add gives it
-// exactly), turns them into those about M:  z log2 e - c = (z - M) log2 e + r.
-// Beside a c past 2^24 r is no longer a fraction (a chunk masked with -1e30 has
-// one of 1e21, and S would be 0 or infinite): the careful form then.
+// log S nor T / S is larger than it has to be.  A base that needs no exchange
+// between lanes (lane 0's maximum: 405 us where this takes 409) lets both grow
+// to some 13 in rows whose top stands out, and they lose that many digits to
+// each other: 1.5e-5 of an entropy, 3e-6 of a log probability, 2e-6 and 8e-7
+// here (3,000 rows with a top 2 to 14 above the rest).  With c = fp32(M log2 e)
+// the sums are about c in log2 units, z log2 e - c one fused multiply-add; r,
+// the rounding error of c (a fused multiply-add gives it exactly), turns them
+// into those about M:  z log2 e - c = (z - M) log2 e + r.  Beside a c past 2^24
+// r is no longer a fraction (a chunk masked with -1e30 has one of 1e21, and S
+// would be 0 or infinite): the careful form then.
 __device__ __forceinline__ LpSum lp_chunk_sum(const float (&z)[kLpPer], float m) {
   const float M = lp_wave_max(m);
   const float c = M * kLog2e;
@@ -771,8 +775,8 @@ static int lp_strips(bool f32, int64_t vocab) {
 
 // Rows of a tile: 8 to 32, about 2,048 workgroups in all.  (8,192 x 131,072
 // bf16 on one GPU: 777 us with tiles of 32, 820 with 16 or 64; 864 with 128.)  A rule of the
-// sizes alone (the type's strip width aside: the narrower is taken for both),
-// so the order of dscale's sums is too.
+// sizes alone (the type's strip width aside: bf16's, the wider, counts for
+// both), so the order of dscale's sums is too.
 static int lp_tile_rows(int64_t rows, int64_t vocab) {
   const int64_t want = rows * lp_strips(false, vocab) / 2048;
   int t = 8;
