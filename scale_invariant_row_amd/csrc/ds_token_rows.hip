@@ -17,22 +17,8 @@ namespace {
 
 using namespace dsh;
 
-constexpr int64_t kMostBytes = INT64_MAX / 8;
 constexpr int64_t kMostGradRows = 1 << 30;   // of an embedding's gradient
 constexpr int64_t kMostGradBytes = 400ll << 30;   // of its table and of its rows (a grid's limit)
-
-bool type_ok(int32_t t) { return t == DS_TYPE_BF16 || t == DS_TYPE_F32; }
-int64_t type_bytes(int32_t t) { return t == DS_TYPE_F32 ? 4 : 2; }
-bool id_bytes_ok(int32_t b) { return b == 4 || b == 8; }
-
-// A workspace of `need` bytes: given, aligned, and clear of the call's buffers.
-int check_workspace(const void* ws, int64_t have, int64_t need) {
-  if (need == 0) return DS_OK;
-  if (ws == nullptr) return DS_ERR_NULL;
-  if (have < need) return DS_ERR_WORKSPACE;
-  if (!aligned(ws, 16)) return DS_ERR_ALIGN;
-  return DS_OK;
-}
 
 // Shape and types shared by an embedding's two directions.
 int check_embed(int32_t type, int64_t vocab, int32_t id_bytes, float scale, int64_t rows,
@@ -129,13 +115,6 @@ int ds_embed_rows_backward(const uint16_t* dy, const void* ids, int32_t id_bytes
 
 namespace {
 
-// One strided [rows, width] bf16 buffer of a q/k call.
-struct View {
-  const void* p;
-  int64_t ld, width;
-  bool out;
-};
-
 int check_qk(int64_t rows, int32_t nq, int32_t nk, int32_t head_dim, float eps, int64_t* wq,
              int64_t* wk) {
   if (rows < 0 || nq < 0 || nk < 0) return DS_ERR_SHAPE;
@@ -144,36 +123,6 @@ int check_qk(int64_t rows, int32_t nq, int32_t nk, int32_t head_dim, float eps, 
   *wq = (int64_t)nq * head_dim;
   *wk = (int64_t)nk * head_dim;
   return *wq > (1 << 24) || *wk > (1 << 24) ? DS_ERR_SHAPE : DS_OK;
-}
-
-// The views of a call (those of no heads have width 0 and are skipped): given,
-// aligned, wide enough, and no output sharing an element with anything else,
-// but for `in_place` pairs (index of an output, index of the buffer it may be).
-template <int N>
-int check_views(const View (&v)[N], int64_t rows, const int (*in_place)[2], int n_in_place,
-                const void* const* vecs, const size_t* vec_bytes, int n_vecs) {
-  for (const View& a : v)
-    if (a.width > 0 && a.p == nullptr) return DS_ERR_NULL;
-  for (const View& a : v)
-    if (a.width > 0 && (a.ld < a.width || a.ld % 8 != 0 || rows > kMostBytes / 2 / a.ld))
-      return DS_ERR_SHAPE;
-  for (const View& a : v)
-    if (a.width > 0 && !aligned(a.p, 16)) return DS_ERR_ALIGN;
-  for (int i = 0; i < N; ++i) {
-    if (!v[i].out || v[i].width == 0) continue;
-    const size_t nb = span_bytes(rows, v[i].ld, v[i].width);
-    for (int k = 0; k < n_vecs; ++k)
-      if (vecs[k] != nullptr && overlaps(v[i].p, nb, vecs[k], vec_bytes[k])) return DS_ERR_ARG;
-    for (int j = 0; j < N; ++j) {
-      if (j == i || v[j].width == 0) continue;
-      bool may = false;
-      for (int k = 0; k < n_in_place; ++k) may = may || (in_place[k][0] == i && in_place[k][1] == j);
-      if (may && v[i].p == v[j].p && v[i].ld == v[j].ld) continue;
-      if (views_overlap(v[i].p, v[i].ld, v[i].width, v[j].p, v[j].ld, v[j].width, rows))
-        return DS_ERR_ARG;
-    }
-  }
-  return DS_OK;
 }
 
 }  // namespace
@@ -335,26 +284,6 @@ int check_logits(int32_t type, int64_t ld, float inv_temp, int32_t label_bytes, 
 // Bytes that [rows, vocab] logits of row stride ld span.
 size_t logits_span(int32_t type, int64_t rows, int64_t ld, int64_t vocab) {
   return rows == 0 ? 0 : ((size_t)(rows - 1) * (size_t)ld + (size_t)vocab) * (size_t)type_bytes(type);
-}
-
-struct Buf {
-  const void* p;
-  size_t bytes;
-};
-
-// No output shares a byte with an input or with another output.
-template <int NO, int NI>
-bool apart(const Buf (&outs)[NO], const Buf (&ins)[NI]) {
-  for (int i = 0; i < NO; ++i) {
-    if (outs[i].p == nullptr) continue;
-    for (int j = 0; j < NI; ++j)
-      if (ins[j].p != nullptr && overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
-        return false;
-    for (int j = 0; j < i; ++j)
-      if (outs[j].p != nullptr && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
-        return false;
-  }
-  return true;
 }
 
 }  // namespace

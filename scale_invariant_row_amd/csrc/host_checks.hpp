@@ -2,7 +2,7 @@
 // tests, the grid cap and launches in pieces.
 #pragma once
 
-#include "ds_rows.h"
+#include "ds_token_rows.h"
 
 #include <hip/hip_runtime.h>
 
@@ -117,6 +117,78 @@ inline bool views_overlap(const void* a, int64_t lda, int64_t wa, const void* b,
     if (t > de - wa && t < de + wb) return true;
   }
   return false;
+}
+
+constexpr int64_t kMostBytes = INT64_MAX / 8;
+
+inline bool type_ok(int32_t t) { return t == DS_TYPE_BF16 || t == DS_TYPE_F32; }
+inline int64_t type_bytes(int32_t t) { return t == DS_TYPE_F32 ? 4 : 2; }
+inline bool id_bytes_ok(int32_t b) { return b == 4 || b == 8; }
+
+// A workspace of `need` bytes: given, aligned, and clear of the call's buffers.
+inline int check_workspace(const void* ws, int64_t have, int64_t need) {
+  if (need == 0) return DS_OK;
+  if (ws == nullptr) return DS_ERR_NULL;
+  if (have < need) return DS_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return DS_ERR_ALIGN;
+  return DS_OK;
+}
+
+// One strided [rows, width] bf16 buffer of a call on heads.
+struct View {
+  const void* p;
+  int64_t ld, width;
+  bool out;
+};
+
+// The views of a call (those of no heads have width 0 and are skipped): given,
+// aligned, wide enough, and no output sharing an element with anything else,
+// but for `in_place` pairs (index of an output, index of the buffer it may be).
+template <int N>
+int check_views(const View (&v)[N], int64_t rows, const int (*in_place)[2], int n_in_place,
+                const void* const* vecs, const size_t* vec_bytes, int n_vecs) {
+  for (const View& a : v)
+    if (a.width > 0 && a.p == nullptr) return DS_ERR_NULL;
+  for (const View& a : v)
+    if (a.width > 0 && (a.ld < a.width || a.ld % 8 != 0 || rows > kMostBytes / 2 / a.ld))
+      return DS_ERR_SHAPE;
+  for (const View& a : v)
+    if (a.width > 0 && !aligned(a.p, 16)) return DS_ERR_ALIGN;
+  for (int i = 0; i < N; ++i) {
+    if (!v[i].out || v[i].width == 0) continue;
+    const size_t nb = span_bytes(rows, v[i].ld, v[i].width);
+    for (int k = 0; k < n_vecs; ++k)
+      if (vecs[k] != nullptr && overlaps(v[i].p, nb, vecs[k], vec_bytes[k])) return DS_ERR_ARG;
+    for (int j = 0; j < N; ++j) {
+      if (j == i || v[j].width == 0) continue;
+      bool may = false;
+      for (int k = 0; k < n_in_place; ++k) may = may || (in_place[k][0] == i && in_place[k][1] == j);
+      if (may && v[i].p == v[j].p && v[i].ld == v[j].ld) continue;
+      if (views_overlap(v[i].p, v[i].ld, v[i].width, v[j].p, v[j].ld, v[j].width, rows))
+        return DS_ERR_ARG;
+    }
+  }
+  return DS_OK;
+}
+
+struct Buf {
+  const void* p;
+  size_t bytes;
+};
+
+// No output shares a byte with an input or with another output.
+template <int NO, int NI>
+bool apart(const Buf (&outs)[NO], const Buf (&ins)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    if (outs[i].p == nullptr) continue;
+    for (int j = 0; j < NI; ++j)
+      if (ins[j].p != nullptr && overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+        return false;
+    for (int j = 0; j < i; ++j)
+      if (outs[j].p != nullptr && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return false;
+  }
+  return true;
 }
 
 }  // namespace dsh
