@@ -1,5 +1,5 @@
-"""ctypes binding of libdsrows.so (include/ds_rows.h, include/ds_token_rows.h):
-argument marshalling only.
+"""ctypes binding of libdsrows.so (include/ds_rows.h, include/ds_token_rows.h,
+include/ds_decode_rows.h): argument marshalling only.
 
 Every computation runs in the library's HIP kernels.  The functions take
 torch tensors on a HIP device, check dtype/shape/contiguity/device, pass raw
@@ -25,6 +25,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("DS_ROWS_LIB") or os.path.join(PKG, "_lib", "libdsrows.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "ds_rows.h")
 TOKEN_HEADER = os.path.join(os.path.dirname(PKG), "include", "ds_token_rows.h")
+DECODE_HEADER = os.path.join(os.path.dirname(PKG), "include", "ds_decode_rows.h")
 
 DS_OK = 0
 DS_ERR_NULL = -1
@@ -39,7 +40,9 @@ DS_ERR_SCRATCH = -9
 DS_ERR_WORKSPACE = -10
 DS_SCRATCH_FLOATS = 1 << 20
 DS_MAX_TOP = 32
-DS_TYPE_BF16, DS_TYPE_F32 = 0, 1
+DS_TYPE_BF16, DS_TYPE_F32, DS_TYPE_E4M3 = 0, 1, 2
+DS_MAX_NEW = 16
+DS_MAX_DRAFTS = 32
 
 
 class RownormDesc(ctypes.Structure):
@@ -89,8 +92,31 @@ class RescaleDesc(ctypes.Structure):
     ]
 
 
+class KvCacheDesc(ctypes.Structure):
+    """ds_kv_cache."""
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("ld_table", ctypes.c_int64),
+        ("type", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("n_seqs", ctypes.c_int32),
+        ("pages_per_seq", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _token = None          # the library once ds_token_rows.h's entry points are declared
+_decode = None         # likewise for ds_decode_rows.h's
 _raw_stream = None     # torch's own look-up of a device's current stream, where it has one
 
 
@@ -142,6 +168,17 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def _declare(L, calls, sizes) -> None:
+    for table, res in ((calls, ctypes.c_int), (sizes, ctypes.c_int64)):
+        for name, args in table.items():
+            try:
+                f = getattr(L, name)
+            except AttributeError:
+                raise RuntimeError(f"{LIB_PATH} does not hold {name}: build the library again "
+                                   "with `python -m scale_invariant_row_amd.build`") from None
+            f.argtypes, f.restype = args, res
+
+
 def _token_lib() -> ctypes.CDLL:
     """The library with ds_token_rows.h's entry points declared; raises if the
     loaded build does not hold them."""
@@ -167,17 +204,35 @@ def _token_lib() -> ctypes.CDLL:
             "ds_logprob_rows_workspace": [i64, i64, i32],
             "ds_logprob_rows_backward_workspace": [i64, i64],
         }
-        for table, res in ((sig, ctypes.c_int), (sizes, i64)):
-            for name, args in table.items():
-                try:
-                    f = getattr(L, name)
-                except AttributeError:
-                    raise RuntimeError(f"{LIB_PATH} does not hold {name}: build the library again "
-                                       "with `python -m scale_invariant_row_amd.build`") from None
-                f.argtypes, f.restype = args, res
+        _declare(L, sig, sizes)
         _raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
         _token = L
     return _token
+
+
+def _decode_lib() -> ctypes.CDLL:
+    """The library with ds_decode_rows.h's entry points declared."""
+    global _decode
+    if _decode is None:
+        L = _token_lib()
+        vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+        f64 = ctypes.c_double
+        turned = [vp, i64, vp, i64, vp, vp, i32, i32, f32, vp, i64, vp, i64, i64, i32, i32, i32, vp]
+        _declare(L, {
+            "ds_rope_rows": turned,
+            "ds_rope_rows_backward": turned,
+            "ds_rope_frequencies": [vp, i32, f64, f64, f64, f64, f64],
+            "ds_cache_append_rows": [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, f32, i32,
+                                     vp, vp, f32, vp, i64, i64, i32, vp],
+            "ds_cache_attention_rows": [vp, vp, i64, i32, vp, i32, i32, f32, vp, i64, vp, vp, i64, vp],
+            "ds_draft_verify_rows": [vp, i32, i64, vp, f32, vp, i32, i64, vp, f32, vp, i32, vp, vp,
+                                     vp, vp, vp, i64, i32, i64, vp, i64, vp],
+        }, {
+            "ds_cache_attention_rows_workspace": [vp, i32, i32, i32],
+            "ds_draft_verify_rows_workspace": [i64, i32, i64, i32],
+        })
+        _decode = L
+    return _decode
 
 
 def header_functions(header: str = HEADER) -> List[str]:
@@ -1049,3 +1104,321 @@ def ds_logprob_rows_backward(logits, labels, lse, entropy, dlogp, dentropy=None,
             _ptr(dscale), rows, vocab, _ptr(ws), nbytes, raw)
     _check(st, "ds_logprob_rows_backward")
     return dlogits, dscale
+
+
+# ------------------------------------------------- the rows of a decoding step
+
+def _rope(name, q, k, positions, inv_freq, head_dim, interleaved, amplitude, q_out, k_out, names,
+          stream):
+    torch = _torch()
+    head_dim = int(head_dim)
+    if head_dim <= 0:
+        raise ValueError("head_dim: must be positive")
+    nq = _heads(q, names[0], head_dim)
+    rows = q.shape[0]
+    nk = _heads(k, names[1], head_dim, rows) if k is not None else 0
+    _vec(positions, "positions", rows, torch.int32)
+    _frequencies(inv_freq, head_dim)
+    _like_heads(q_out, q, names[2], head_dim, rows, nq)
+    _like_heads(k_out, k, names[3], head_dim, rows, nk)
+    _on_device_of(q, names[0], **{names[1]: k, "positions": positions, "inv_freq": inv_freq,
+                                  names[2]: q_out, names[3]: k_out})
+    L = _decode_lib()
+    ctx, raw = _launch_on(q, stream)
+    with ctx:
+        if q_out is None:
+            q_out = q.new_empty((rows, nq * head_dim))
+        if k is not None and k_out is None:
+            k_out = k.new_empty((rows, nk * head_dim))
+        st = getattr(L, name)(
+            q.data_ptr(), _row_stride(q), _ptr(k), _row_stride(k), positions.data_ptr(),
+            inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved)), amplitude,
+            q_out.data_ptr(), _row_stride(q_out), _ptr(k_out), _row_stride(k_out), rows, nq, nk,
+            head_dim, raw)
+    _check(st, name)
+    return q_out, k_out
+
+
+def _frequencies(t, head_dim: int):
+    torch = _torch()
+    if t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous() \
+            or not 2 <= 2 * t.shape[0] <= head_dim:
+        raise ValueError(f"inv_freq: expected a contiguous fp32 tensor of 1 to {head_dim // 2} "
+                         "frequencies")
+
+
+def ds_rope_rows(q, k, positions, inv_freq, head_dim: int, interleaved: bool = False,
+                 amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions on q [rows, nq * head_dim] and k [rows, nk * head_dim] (k may be None).
+
+    The first ``2 * len(inv_freq)`` values of each head turn, as halves or
+    (``interleaved``) as neighbouring pairs, their cos and sin times
+    ``amplitude``; the others are copied.  ``q``/``k`` may be strided row
+    views; ``positions``: int32 [rows]; ``inv_freq``: fp32.  Returns
+    (q_out, k_out); the outputs may be the inputs themselves.
+    """
+    return _rope("ds_rope_rows", q, k, positions, inv_freq, head_dim, interleaved, amplitude, q_out,
+                 k_out, ("q", "k", "q_out", "k_out"), stream)
+
+
+def ds_rope_rows_backward(dq_out, dk_out, positions, inv_freq, head_dim: int,
+                          interleaved: bool = False, amplitude: float = 1.0, dq=None, dk=None,
+                          stream=None):
+    """The gradient of ds_rope_rows from the gradients reaching its outputs:
+    (dq, dk), which may be ``dq_out`` and ``dk_out`` themselves."""
+    return _rope("ds_rope_rows_backward", dq_out, dk_out, positions, inv_freq, head_dim, interleaved,
+                 amplitude, dq, dk, ("dq_out", "dk_out", "dq", "dk"), stream)
+
+
+def ds_rope_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1.0,
+                        original: float = 1.0, low: float = 0.0, high: float = 0.0, device=None):
+    """inv_freq (fp32 [rotary_dim / 2]) for ds_rope_rows.
+
+    For a context ``factor`` times the ``original`` positions: pairs that turn
+    more than ``high`` times over those keep their frequency, pairs that turn
+    fewer than ``low`` times are slowed by the factor, those between in part;
+    with low and high 0 every pair is slowed.
+    """
+    torch = _torch()
+    rotary_dim = int(rotary_dim)
+    f = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.float32)
+    _check(_decode_lib().ds_rope_frequencies(f.data_ptr(), rotary_dim, base, factor, original, low,
+                                             high), "ds_rope_frequencies")
+    return f if device is None else f.to(device)
+
+
+class KvCache:
+    """A paged cache of keys and values, as ds_cache_append_rows and
+    ds_cache_attention_rows take it.
+
+    ``k``, ``v``: [pages, page_size, heads, head_dim] views of any order in
+    memory (one order for both, unit stride along head_dim), bf16 or
+    float8_e4m3fn (torch.uint8 for its bit patterns); ``page_table``: int32
+    [seqs, pages_per_seq], whose page t / page_size holds token t, a page
+    outside the cache (-1) none; ``k_scale``, ``v_scale``: fp32 [heads] or
+    None, what a stored value is to be multiplied by.  The tensors stay the
+    caller's; their contents may change between calls.
+    """
+    __slots__ = ("k", "v", "page_table", "k_scale", "v_scale", "desc", "_at", "_workspace")
+
+    def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
+        torch = _torch()
+        types = {torch.bfloat16: DS_TYPE_BF16, torch.int16: DS_TYPE_BF16, torch.uint16: DS_TYPE_BF16,
+                 torch.float8_e4m3fn: DS_TYPE_E4M3, torch.uint8: DS_TYPE_E4M3}
+        for t, n in ((k, "k"), (v, "v")):
+            if t.dtype not in types:
+                raise TypeError(f"{n}: expected bf16 or e4m3 data, got {t.dtype}")
+            if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+                raise ValueError(f"{n}: expected a [pages, page_size, heads, head_dim] tensor with "
+                                 "unit stride along head_dim")
+        if v.dtype != k.dtype or v.shape != k.shape:
+            raise ValueError("v: must be like k")
+        # the stride of a dimension of one says nothing
+        strides = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        if strides != [v.stride(i) if v.shape[i] > 1 else 0 for i in range(3)]:
+            raise ValueError("v: must be laid out like k")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 \
+                or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table: expected an int32 [seqs, pages_per_seq] tensor with unit "
+                             "column stride")
+        pages, page_size, heads, head_dim = k.shape
+        _vec(k_scale, "k_scale", heads, torch.float32)
+        _vec(v_scale, "v_scale", heads, torch.float32)
+        for t, n in ((v, "v"), (page_table, "page_table"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{n}: must be on the device of k")
+        self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
+        seqs, per_seq = page_table.shape
+        self.desc = KvCacheDesc(
+            k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), *strides,
+            page_table.stride(0) if seqs > 1 else per_seq, types[k.dtype], pages, page_size, heads,
+            head_dim, seqs, per_seq)
+        self._at = ctypes.addressof(self.desc)
+        self._workspace = {}
+
+    def _attention_workspace(self, *sizes) -> int:
+        n = self._workspace.get(sizes)
+        if n is None:
+            n = _decode_lib().ds_cache_attention_rows_workspace(self._at, *sizes)
+            if n < 0:
+                _check(n, "ds_cache_attention_rows")
+            self._workspace[sizes] = n
+        return n
+
+
+def ds_cache_append_rows(cache: KvCache, k, v, positions, seqs=None, inv_freq=None,
+                         interleaved: bool = False, amplitude: float = 1.0, q=None,
+                         rms_eps: Optional[float] = None, q_weight=None, k_weight=None, q_out=None,
+                         stream=None):
+    """Puts each row's keys and values into the cache at its sequence's position.
+
+    ``k``, ``v``: bf16 [rows, heads * head_dim] (rows may be strided);
+    ``positions``: int32 [rows]; ``seqs``: int32 [rows], or None for equally
+    many rows of each sequence in turn.  With ``rms_eps`` the heads of k (and
+    q) are RMS normed first, times ``k_weight`` (``q_weight``), fp32
+    [head_dim] or None; with ``inv_freq`` they are rotated as by ds_rope_rows.
+    A row outside the cache stores nothing.  With ``q`` its heads, normed and
+    rotated, are returned (``q_out``, which may be q); None otherwise.
+    """
+    torch = _torch()
+    desc = cache.desc
+    heads, head_dim = desc.n_heads, desc.head_dim
+    if head_dim <= 0:
+        raise ValueError("cache: has no head_dim")
+    if _heads(k, "k", head_dim) != heads:
+        raise ValueError(f"k: expected {heads} heads of {head_dim}")
+    rows = k.shape[0]
+    for t, n in ((v, "v"), (q, "q"), (q_out, "q_out")):
+        if t is not None and t.shape[0] != rows:
+            raise ValueError(f"{n}: expected {rows} rows like k, got {t.shape[0]}")
+    if _heads(v, "v", head_dim) != heads:
+        raise ValueError(f"v: expected {heads} heads of {head_dim}")
+    nq = 0 if q is None else _heads(q, "q", head_dim)
+    if q_out is not None and (q is None or _heads(q_out, "q_out", head_dim) != nq):
+        raise ValueError("q_out: expected q's heads")
+    _vec(positions, "positions", rows, torch.int32)
+    _vec(seqs, "seqs", rows, torch.int32)
+    if seqs is None and (desc.n_seqs == 0 or rows % desc.n_seqs):
+        raise ValueError(f"seqs: needed, {rows} rows are no multiple of {desc.n_seqs} sequences")
+    if inv_freq is not None:
+        _frequencies(inv_freq, head_dim)
+    if rms_eps is None and not (q_weight is None and k_weight is None):
+        raise ValueError("rms_eps: weights need it")
+    _vec(q_weight, "q_weight", head_dim, torch.float32)
+    _vec(k_weight, "k_weight", head_dim, torch.float32)
+    _on_device_of(cache.k, "cache", k=k, v=v, positions=positions, seqs=seqs, inv_freq=inv_freq, q=q,
+                  q_weight=q_weight, k_weight=k_weight, q_out=q_out)
+    L = _decode_lib()
+    ctx, raw = _launch_on(k, stream)
+    with ctx:
+        if q is not None and q_out is None:
+            q_out = q.new_empty((rows, nq * head_dim))
+        st = L.ds_cache_append_rows(
+            cache._at, _ptr(q), _row_stride(q), k.data_ptr(), _row_stride(k), v.data_ptr(),
+            _row_stride(v), positions.data_ptr(), _ptr(seqs), _ptr(inv_freq),
+            0 if inv_freq is None else 2 * inv_freq.shape[0], int(bool(interleaved)), amplitude,
+            int(rms_eps is not None), _ptr(q_weight), _ptr(k_weight),
+            0.0 if rms_eps is None else rms_eps, _ptr(q_out), _row_stride(q_out), rows, nq, raw)
+    _check(st, "ds_cache_append_rows")
+    return q_out
+
+
+def ds_cache_attention_rows(cache: KvCache, q, lens, scale: Optional[float] = None, window: int = 0,
+                            out=None, want_lse: bool = False, stream=None):
+    """Attention of each sequence's newest tokens over its cached ones.
+
+    ``q``: bf16 [seqs * new_tokens, nq * head_dim], the rows of a sequence
+    together in their order (rows may be strided); ``lens``: int32 [seqs], the
+    tokens each sequence holds, the new ones included.  A row sees the tokens
+    up to its own, the last ``window`` of them if that is not 0; ``scale``:
+    1 / sqrt(head_dim) if not given.  Returns out (bf16, like q), or (out, lse)
+    with fp32 lse [rows, nq]; a row that sees nothing gets 0 and -infinity.
+    """
+    torch = _torch()
+    desc = cache.desc
+    head_dim, seqs = desc.head_dim, desc.n_seqs
+    if head_dim <= 0:
+        raise ValueError("cache: has no head_dim")
+    nq = _heads(q, "q", head_dim)
+    rows = q.shape[0]
+    if nq == 0 or nq % max(desc.n_heads, 1):
+        raise ValueError(f"q: its heads must be a multiple of the cache's {desc.n_heads}")
+    if rows % max(seqs, 1) or (rows == 0) != (seqs == 0):
+        raise ValueError(f"q: expected equally many rows of each of {seqs} sequences, got {rows}")
+    new = rows // seqs if seqs else 1
+    if new > DS_MAX_NEW:
+        raise ValueError(f"q: at most {DS_MAX_NEW} new tokens a sequence")
+    _vec(lens, "lens", seqs, torch.int32)
+    window = int(window)
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window: must not be negative")
+    if out is not None and (_heads(out, "out", head_dim, rows) != nq):
+        raise ValueError(f"out: expected [{rows}, {nq * head_dim}]")
+    _on_device_of(cache.k, "cache", q=q, lens=lens, out=out)
+    L = _decode_lib()
+    nbytes = cache._attention_workspace(nq, new, window)
+    ctx, raw = _launch_on(q, stream)
+    with ctx:
+        if out is None:
+            out = q.new_empty((rows, nq * head_dim))
+        lse = q.new_empty((rows, nq), dtype=torch.float32) if want_lse else None
+        ws = _workspace(nbytes, q)
+        st = L.ds_cache_attention_rows(
+            cache._at, q.data_ptr(), _row_stride(q), nq, lens.data_ptr(), new, window,
+            head_dim ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out), _ptr(lse),
+            _ptr(ws), nbytes, raw)
+    _check(st, "ds_cache_attention_rows")
+    return (out, lse) if want_lse else out
+
+
+class DraftVerify(NamedTuple):
+    """What ds_draft_verify_rows returns: int32 [seqs]; int32 and fp32
+    [seqs, drafts + 1]."""
+    accepted: object
+    tokens: object
+    logp: object
+
+
+def ds_draft_verify_rows(target, drafted, u_accept, u_sample, draft=None, scale=None,
+                         inv_temp: float = 1.0, draft_scale=None, draft_inv_temp: float = 1.0,
+                         stream=None) -> DraftVerify:
+    """Accepts drafted tokens with the target's own probabilities, and samples
+    the token that follows them.
+
+    ``target``: logits [seqs * (drafts + 1), vocab]; ``draft``: the draft
+    model's [seqs * drafts, vocab], or None where each draft was certain
+    (fp32 or bf16, rows may be strided); each with a column ``scale`` (fp32
+    [vocab] or None) and an inverse temperature, as in ds_logprob_rows.
+    ``drafted``: int32 or int64 [seqs, drafts], an id outside the vocabulary
+    ends a sequence's drafts; ``u_accept``, ``u_sample``: fp32 random numbers
+    in [0, 1), [seqs, drafts] and [seqs].  ``tokens``: the accepted, the next,
+    then -1; ``logp``: the target's log probability of each.
+    """
+    torch = _torch()
+    kind, t_rows, vocab, ldt = _logits(target, "target")
+    if drafted.dtype not in (torch.int32, torch.int64) or drafted.dim() != 2 \
+            or not drafted.is_contiguous():
+        raise ValueError("drafted: expected a contiguous int32 or int64 [seqs, drafts] tensor")
+    seqs, drafts = drafted.shape
+    if drafts > DS_MAX_DRAFTS:
+        raise ValueError(f"drafted: at most {DS_MAX_DRAFTS} a sequence")
+    if t_rows != seqs * (drafts + 1):
+        raise ValueError(f"target: expected {seqs * (drafts + 1)} rows, got {t_rows}")
+    if u_accept.dtype != torch.float32 or tuple(u_accept.shape) != (seqs, drafts) \
+            or not u_accept.is_contiguous():
+        raise ValueError(f"u_accept: expected a contiguous fp32 [{seqs}, {drafts}] tensor")
+    _vec(u_sample, "u_sample", seqs, torch.float32)
+    dkind, ldd = kind, vocab
+    if draft is not None:
+        dkind, d_rows, d_vocab, ldd = _logits(draft, "draft")
+        if d_rows != seqs * drafts or d_vocab != vocab:
+            raise ValueError(f"draft: expected [{seqs * drafts}, {vocab}]")
+    else:
+        draft_scale = None                       # no draft logits to scale
+    _vec(scale, "scale", vocab, torch.float32)
+    _vec(draft_scale, "draft_scale", vocab, torch.float32)
+    _on_device_of(target, "target", drafted=drafted, u_accept=u_accept, u_sample=u_sample, draft=draft,
+                  scale=scale, draft_scale=draft_scale)
+    L = _decode_lib()
+    nbytes = _verify_workspace(seqs, drafts, vocab, int(draft is not None and drafts > 0))
+    ctx, raw = _launch_on(target, stream)
+    with ctx:
+        accepted = target.new_empty(seqs, dtype=torch.int32)
+        tokens = target.new_empty((seqs, drafts + 1), dtype=torch.int32)
+        logp = target.new_empty((seqs, drafts + 1), dtype=torch.float32)
+        ws = _workspace(nbytes, target)
+        st = L.ds_draft_verify_rows(
+            target.data_ptr(), kind, ldt, _ptr(scale), inv_temp, _ptr(draft), dkind, ldd,
+            _ptr(draft_scale), draft_inv_temp, drafted.data_ptr(), drafted.element_size(),
+            u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(), tokens.data_ptr(),
+            logp.data_ptr(), seqs, drafts, vocab, _ptr(ws), nbytes, raw)
+    _check(st, "ds_draft_verify_rows")
+    return DraftVerify(accepted, tokens, logp)
+
+
+@functools.lru_cache(maxsize=4096)
+def _verify_workspace(*sizes) -> int:
+    n = _decode_lib().ds_draft_verify_rows_workspace(*sizes)
+    if n < 0:
+        _check(n, "ds_draft_verify_rows")
+    return n

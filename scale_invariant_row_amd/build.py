@@ -26,7 +26,8 @@ BENCH_SOURCES = ["bench_stream.hip"]
 SOURCES = ["ds_rows.hip", "inst_l2.hip", "inst_slerp.hip", "inst_rownorm.hip",
            "inst_l2_bwd.hip", "inst_rownorm_bwd.hip", "inst_act.hip", "inst_qk.hip",
            "inst_rescale.hip", "inst_rms.hip", "inst_rms_bwd.hip", "inst_colblock.hip",
-           "ds_token_rows.hip", "token_embed.hip", "token_qk_rms.hip", "token_logprob.hip"]
+           "ds_token_rows.hip", "token_embed.hip", "token_qk_rms.hip", "token_logprob.hip",
+           "ds_decode_rows.hip", "decode_heads.hip", "decode_attention.hip", "decode_verify.hip"]
 ARCH = "gfx950"
 
 # -ffp-contract=off: only explicit fmaf fuses (the slerp lerp is three
