@@ -8,11 +8,13 @@
 // A head spreads over LPH lanes, two 16-byte vectors of 8 values a lane.  Which
 // two goes by the pairing, so that as a rule a lane holds whole pairs:
 //   halves, R a multiple of 16: vector u of the first R/2 values and the one
-//     that turns with it; past R/16 lanes, 16 values in a row that only pass by
-//   neighbours: 16 values in a row
-//   halves, any other even R: 16 values in a row, and the partners come out of
-//     LDS (a wave's heads, 4 KB)
-// so loads and stores stay 16 bytes wide for every R.  A value that does not
+//     that turns with it; past R/16 lanes, of the two halves that only pass by
+//   neighbours: vector u of the head's first half and of its second
+//   halves, any other even R: the same two, and the partners come out of LDS (a
+//     wave's heads, 4 KB)
+// so loads and stores stay 16 bytes wide for every R, and neighbouring lanes
+// touch neighbouring vectors (two vectors in a row a lane, every load and store
+// taking half of each line, held 16,384 rows of 32 + 8 heads of 128 at 94 us).  A value that does not
 // turn is never multiplied (an infinity beside it would make a NaN of it).
 #include "decode_launch.hpp"
 #include "token_heads.hpp"
@@ -29,15 +31,13 @@ struct Place {
   __device__ __forceinline__ Place(int lane, int hd, int rotary) {
     u = lane % LPH;
     active = u * 16 < hd;
-    a = 16 * u;
-    b = a + 8;
+    a = 8 * u;
+    b = hd / 2 + 8 * u;
     turns = true;
     if constexpr (PAIRS == kHalves) {
       turns = u * 16 < rotary;
-      if (turns) {
-        a = 8 * u;
-        b = rotary / 2 + 8 * u;
-      }
+      a = turns ? 8 * u : rotary / 2 + 8 * u;
+      b = turns ? rotary / 2 + 8 * u : hd / 2 + 8 * u;
     }
   }
 };
@@ -71,7 +71,7 @@ __device__ __forceinline__ void lane_angles(const float (&cs)[2][128], const Pla
   if constexpr (PAIRS == kOddHalves) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int i = 8 * at.u + j;
+    const int i = PAIRS == kHalves ? 8 * at.u + j : (j < 4 ? at.a : at.b) / 2 + j % 4;
     const bool in = 2 * i < rotary;
     c[j] = in ? cs[0][i] : 1.f;
     s[j] = in ? cs[1][i] : 0.f;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void turn16(float (&v)[16], const float (&c)[8], cons
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = v[2 * j], y = v[2 * j + 1];
-      const bool in = 16 * at.u + 2 * j < rotary;
+      const bool in = (j < 4 ? at.a : at.b) + 2 * (j % 4) < rotary;
       v[2 * j] = in ? x * c[j] - y * s[j] : x;
       v[2 * j + 1] = in ? y * c[j] + x * s[j] : y;
     }
@@ -105,14 +105,14 @@ __device__ __forceinline__ void turn16(float (&v)[16], const float (&c)[8], cons
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     if (at.active) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) head[16 * at.u + j] = v[j];
+      for (int j = 0; j < 16; ++j) head[(j < 8 ? at.a : at.b) + j % 8] = v[j];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (at.active) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int e = 16 * at.u + j;
+        const int e = (j < 8 ? at.a : at.b) + j % 8;
         if (e < rotary) {
           const bool first = e < half;
           const int i = first ? e : e - half;
