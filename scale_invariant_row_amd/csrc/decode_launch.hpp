@@ -153,6 +153,6 @@ struct VerifyArgs {
 };
 int64_t verify_slices(int drafts, int64_t vocab, bool with_draft);   // of one sequence
 int64_t verify_workspace(int64_t seqs, int drafts, int64_t vocab, bool with_draft);
-hipError_t launch_draft_verify(const VerifyArgs& a, void* workspace, hipStream_t stream);
+hipError_t launch_draft_verify(const VerifyArgs& a, int cus, void* workspace, hipStream_t stream);
 
 }  // namespace dsr

@@ -410,7 +410,7 @@ int ds_draft_verify_rows(const void* target, int32_t target_type, int64_t ldt, c
   a.drafts = n_drafts;
   a.vocab = (int32_t)vocab;
   (void)hipGetLastError();
-  return launch_status(dsr::launch_draft_verify(a, workspace, (hipStream_t)stream));
+  return launch_status(dsr::launch_draft_verify(a, cus, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"
