@@ -9,10 +9,9 @@
 // the matrix instruction (16 x 16 x 32): S^T = K Q^T has a lane hold 4 keys of
 // one row, which is how P^T has to lie for O^T = V^T P^T, so P never leaves its
 // lane.  V^T's 8 keys of one dimension a lane come out of LDS transposed
-// (ds_read_tr16).  A wave takes 32 keys at a time; a workgroup's four waves
-// share out a chunk of the sequence and join at its end; chunks of one sequence
-// are joined by a second kernel.  How a sequence is cut goes by its own length
-// alone, so a row's bits do not depend on the batch.
+// (ds_read_tr16).  A wave takes a chunk of a sequence, 32 keys at a time; the
+// chunks of a sequence are joined by a second kernel.  How a sequence is cut goes
+// by its own length alone, so a row's bits do not depend on the batch.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,12 +31,12 @@ struct Split {
   float* sums;                       // [row][head][max_chunks][hd]
   float* stats;                      // [row][head][max_chunks][2]: m (of z log2 e), l
   int32_t max_chunks;
-  int32_t workers;                   // workgroups a sequence, kv head and row group
   int32_t row_groups;
 };
 
-__device__ __forceinline__ int32_t scalar_load(const int32_t* p) {
-  return *(const __attribute__((address_space(4))) int32_t*)p;
+template <class T>
+__device__ __forceinline__ T scalar_load(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
 }
 
 __device__ __forceinline__ Span span_here(const AttendArgs& a, int seq) {
@@ -68,155 +67,214 @@ __device__ __forceinline__ u32x2_t widen4(uint32_t w) {
   return u32x2_t{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
 }
 
-// HB: head_dim in blocks of 32, rounded up.  RT: tiles of 16 rows a workgroup.
+// The work is a list of chunks: of sequence 0 its heads' (and row groups'), one
+// after the other, then of sequence 1.  Wave i of W takes the i-th of W equal
+// stretches of the list, so as many waves as the chip holds are busy for as long
+// whatever the lengths are.
+struct Item {
+  int seq, part, c;                  // part: row group * heads + head; c: chunk
+  Span span;                         // of the sequence
+};
+
+// The number of chunks (of one part) of sequence s0 + lane, 0 past the last.
+__device__ __forceinline__ int chunks_of(const AttendArgs& a, int s0, int lane) {
+  if (s0 + lane >= a.cache.seqs) return 0;
+  const int len = a.lens[s0 + lane], cap = a.cache.pages_per_seq << a.cache.page_shift;
+  return span_of(len < 0 ? 0 : len > cap ? cap : len, a.n_new, a.window).n;
+}
+
+__device__ __forceinline__ int64_t list_length(const AttendArgs& a, int parts, int lane) {
+  int sum = 0;
+  for (int s0 = 0; s0 < a.cache.seqs; s0 += 64) sum += chunks_of(a, s0, lane);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  return (int64_t)__builtin_amdgcn_readfirstlane(sum) * parts;
+}
+
+// The item at place `at` of the list.
+__device__ __forceinline__ Item item_at(const AttendArgs& a, int parts, int64_t at, int lane) {
+  Item it{0, 0, 0, {}};
+  int before = 0;                                          // chunks of the sequences before these 64
+  for (int s0 = 0; s0 < a.cache.seqs; s0 += 64) {
+    const int n = chunks_of(a, s0, lane);
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int t = __shfl_up(upto, d);
+      if (lane >= d) upto += t;
+    }
+    upto += before;
+    const uint64_t past = __builtin_amdgcn_ballot_w64(at < (int64_t)upto * parts);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      it.seq = s0 + l;
+      before = __builtin_amdgcn_readlane(upto - n, l);
+      break;
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+  it.span = span_here(a, it.seq);
+  const int rest = (int)(at - (int64_t)before * parts);
+  it.part = rest / it.span.n;
+  it.c = rest % it.span.n;
+  return it;
+}
+
+// HB: head_dim in blocks of 32, rounded up.  RT: tiles of 16 rows a wave.
 //
-// A wave walks its tiles of 32 keys, across the chunks of its workgroup, one
-// ahead with its loads: the next tile's K is asked for as soon as this one's has
-// gone into S, its V as soon as this one's is in LDS, the page of the one after
-// before either.  Nothing but the join of a chunk waits for another wave.
+// A wave walks the tiles of 32 keys of its chunks, one ahead with its loads: the
+// next tile's K is asked for as soon as this one's has gone into S, its V as soon
+// as this one's is in LDS, the page of the one after before either.  No wave
+// waits for another.
 template <int HB, bool E4M3, int RT>
-__global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_kernel(const AttendArgs a, const Split sp) {
+__global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_kernel(const AttendArgs a,
+                                                                                    const Split sp) {
   constexpr int HP = HB * 32, DB = HB * 2;                 // padded head_dim; its blocks of 16
   constexpr int VS = HP + 16;                              // bf16 a row of V in LDS: rows start 8 banks apart
-  constexpr int OS = HP + 4;                               // floats a row of O
   constexpr int VP = E4M3 ? HB : 2 * HB, PPR = E4M3 ? 2 * HB : 4 * HB;   // V's 16-byte pieces a lane, a row
-  constexpr int kVBytes = 4 * kTile * VS * 2, kOBytes = 4 * 16 * OS * 4;
-  __shared__ __attribute__((aligned(16))) char pool[kVBytes > kOBytes ? kVBytes : kOBytes];
-  __shared__ int64_t places[4][kTile];                     // byte offset of a key's token, or -1
-  __shared__ float stat[4][RT][16][2];
+  __shared__ __attribute__((aligned(16))) uint16_t v_tiles[4][kTile * VS];
+  __shared__ int64_t places[4][kTile];                     // byte offset of a key's token
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const CacheView& cv = a.cache;
   const int hd = cv.hd;
-  int id = blockIdx.x;
-  const int worker = id % sp.workers;
-  id /= sp.workers;
-  const int group0 = id % sp.row_groups * RT;              // first row tile
-  id /= sp.row_groups;
-  const int head = id % cv.heads, seq = id / cv.heads;
-  const Span span = span_here(a, seq);
-  // this workgroup's chunks
-  const int c_begin = (int)((int64_t)span.n * worker / sp.workers);
-  const int c_end = (int)((int64_t)span.n * (worker + 1) / sp.workers);
-  if (c_begin == c_end) return;
   const int G = a.q_heads / cv.heads, rows = G * a.n_new;
-  if (span.len == 0) {                                     // nothing is seen (and there may be no table)
-    const int first = group0 * 16, n = min(rows - first, RT * 16);
-    for (int i = threadIdx.x; i < n * hd; i += 256) {
-      const int row = first + i / hd, qh = head * G + row % G;
-      const int64_t qr = (int64_t)seq * a.n_new + row / G;
-      a.out[qr * a.ldo + (int64_t)qh * hd + i % hd] = 0;
-      if (i % hd == 0 && a.lse != nullptr) a.lse[qr * a.q_heads + qh] = kNegInf;
-    }
-    return;
-  }
+  const int parts = cv.heads * sp.row_groups;
+  const int64_t total = list_length(a, parts, lane);
+  const int64_t id = (int64_t)blockIdx.x * 4 + wave, ids = (int64_t)gridDim.x * 4;
+  const int64_t list_lo = total * id / ids, list_hi = total * (id + 1) / ids;
+  if (list_lo == list_hi) return;
+  Item item = item_at(a, parts, list_lo, lane);
+  int left = (int)(list_hi - list_lo);                     // items still to do, this one too
 
-  // this lane's row of each tile: its token, and q as the matrix operand
-  int t_row[RT];
-  bf16x8_t q[RT][HB];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = (group0 + r) * 16 + col;
-    const int j = row / G;
-    t_row[r] = span.len - a.n_new + j;
-    // a row past the last takes the first's values, set to 0
-    const uint16_t* p = a.q + ((int64_t)seq * a.n_new + (row < rows ? j : 0)) * a.ldq +
-                        (int64_t)(head * G + (row < rows ? row % G : 0)) * hd;
-#pragma unroll
-    for (int k = 0; k < HB; ++k) {
-      const int d = k * 32 + grp * 8;
-      u32x4_t v = *(const u32x4_t*)(p + min(d, hd - 8));
-      if (row >= rows || d >= hd) v = u32x4_t{0, 0, 0, 0};
-      q[r][k] = __builtin_bit_cast(bf16x8_t, v);
-    }
-  }
-  const int last_row = min(rows, (group0 + RT) * 16) - 1;
-  const int t_first = span.len - a.n_new + group0 * 16 / G, t_last = span.len - a.n_new + last_row / G;
-  const float z_scale = a.scale * (cv.k_scale != nullptr ? cv.k_scale[head] : 1.f) * kLog2e;
-  const float v_scale = cv.v_scale != nullptr ? cv.v_scale[head] : 1.f;
-  const char* kbase = cv.k + head * cv.head_bytes;
-  const char* vbase = cv.v + head * cv.head_bytes;
-  uint16_t* vt = (uint16_t*)pool + wave * kTile * VS;      // this wave's V tile
-  int64_t* place = places[wave];
-
-  // The wave's tiles in order: key `first key`, in chunk `c`; c_end past the last.
+  auto chunk_lo = [](const Item& t) { return t.span.start + t.c * t.span.chunk; };
+  auto next_item = [&](Item& t) {
+    if (++t.c < t.span.n) return;
+    t.c = 0;
+    if (++t.part < parts) return;
+    t.part = 0;
+    ++t.seq;
+    if (t.seq < cv.seqs) t.span = span_here(a, t.seq);
+  };
+  // A tile: the item it is in, how many items come after that one
+  // (-1: there is no such tile), its first key.
   struct Tile {
-    int c, k0;
+    Item it;
+    int after, k0;
   };
-  auto chunk_lo = [&](int c) { return span.start + c * span.chunk; };
-  auto settle = [&](Tile t) {                              // on to the next chunk that has one
-    while (t.c < c_end && t.k0 >= min(span.len, chunk_lo(t.c) + span.chunk)) {
-      ++t.c;
-      t.k0 = chunk_lo(t.c) + wave * kTile;
+  auto settle = [&](Tile& t) {                             // on to the next item that has a tile
+    while (t.after >= 0 && t.k0 >= min(t.it.span.len, chunk_lo(t.it) + t.it.span.chunk)) {
+      if (--t.after < 0) break;
+      next_item(t.it);
+      t.k0 = chunk_lo(t.it);
     }
-    return t;
   };
-  auto first_from = [&](int c) { return settle(Tile{c, chunk_lo(c) + wave * kTile}); };
-  auto after = [&](Tile t) { return settle(Tile{t.c, t.k0 + 4 * kTile}); };
+  auto advance = [&](Tile& t) {
+    t.k0 += kTile;
+    settle(t);
+  };
   // the page of this lane's key (lanes 0..31; of the last key past it)
-  auto ask_page = [&](Tile t) {
-    return cv.table[table_entry(cv, seq, min(t.k0 + (lane & 31), span.len - 1))];
+  auto ask_page = [&](const Tile& t) {
+    const int key = min(t.k0 + (lane & 31), t.it.span.len - 1);
+    return cv.table[t.after >= 0 ? table_entry(cv, t.it.seq, key) : 0];
   };
   typedef std::conditional_t<E4M3, u32x2_t, u32x4_t> kword_t;   // eight values
   kword_t kw[2][HB];                                       // a tile on its way
   u32x4_t vw[VP];
   uint32_t valid = 0;                                      // which of its keys are in the cache and seen
-  auto put_places = [&](Tile t, int32_t page) {
+  uint16_t* vt = v_tiles[wave];
+  int64_t* place = places[wave];
+  auto put_places = [&](const Tile& t, int32_t page) {
     const int key = t.k0 + (lane & 31);
-    const int64_t at = t.c < c_end && key >= span.first && key < span.len ? token_bytes_at(cv, page, key) : -1;
+    const int64_t at =
+        t.after >= 0 && key >= t.it.span.first && key < t.it.span.len ? token_bytes_at(cv, page, key) : -1;
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     if (lane < 32) place[lane] = at < 0 ? 0 : at;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     return (uint32_t)__builtin_amdgcn_ballot_w64(at >= 0);
   };
+  auto head_of = [&](const Item& t) { return t.part < parts ? t.part % cv.heads : 0; };
   // Every lane loads, one without a key of its own the cache's first token (and
   // the first dimensions in place of those past the head): a load under a
   // condition is waited for at once.  What no row sees is masked where it is used.
-  const int past_k = (hd - 1) / 8 * 8;
-  auto ask_k = [&]() {                                     // lane (col, grp): key col, dims 8 grp.. of each 32
+  const int past_k = hd - 8;
+  auto ask_k = [&](const Tile& t) {                        // lane (col, grp): key col, dims 8 grp.. of each 32
+    const char* base = cv.k + head_of(t.it) * cv.head_bytes;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const char* at = kbase + place[half * 16 + col];
+      const char* at = base + place[half * 16 + col];
 #pragma unroll
       for (int k = 0; k < HB; ++k) {
         const int d = min(k * 32 + grp * 8, past_k);
-        if constexpr (E4M3)
-          kw[half][k] = *(const kword_t*)(at + d);
-        else
-          kw[half][k] = *(const kword_t*)(at + d * 2);
+        kw[half][k] = *(const kword_t*)(at + d * (E4M3 ? 1 : 2));
       }
     }
   };
-  auto ask_v = [&]() {                                     // 16 bytes at a time, rows side by side
+  auto ask_v = [&](const Tile& t) {                        // 16 bytes at a time, rows side by side
+    const char* base = cv.v + head_of(t.it) * cv.head_bytes;
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
       const int piece = i * 64 + lane, d = piece % PPR * (E4M3 ? 16 : 8);
-      vw[i] = *(const u32x4_t*)(vbase + place[piece / PPR] + min(d, hd - (E4M3 ? 16 : 8)) * (E4M3 ? 1 : 2));
+      vw[i] = *(const u32x4_t*)(base + place[piece / PPR] + min(d, hd - (E4M3 ? 16 : 8)) * (E4M3 ? 1 : 2));
     }
   };
-  Tile cur = first_from(c_begin), ahead = after(cur);
+  Tile cur, ahead;
   int32_t page_ahead;
-  auto prime = [&]() {                                     // the loads of `cur`, the page of `ahead`
+  auto prime = [&]() {                                     // from `item` on: the loads of `cur`, the page of `ahead`
+    cur = Tile{item, left - 1, chunk_lo(item)};
+    settle(cur);
+    ahead = cur;
+    advance(ahead);
     const int32_t page = ask_page(cur);
     page_ahead = ask_page(ahead);
     valid = put_places(cur, page);
     // K's loads before V's, as in the loop, and on every way into it: how many
     // younger loads a tile may leave on their way there is the least of them all
     __builtin_amdgcn_sched_barrier(0);
-    ask_k();
+    ask_k(cur);
     __builtin_amdgcn_sched_barrier(0);
-    ask_v();
+    ask_v(cur);
     __builtin_amdgcn_sched_barrier(0);
   };
   prime();
 
+  int t_row[RT];                                           // this lane's row of each row tile: its token
+  bf16x8_t q[RT][HB];                                      // and its q, as the matrix operand
+  int q_seq = -1, q_part = -1;
   // A second pass over a chunk is for sums that came out infinite or NaN: where V
   // holds an infinity, its products with the two parts of a P may cancel to NaN,
   // so the lanes with such sums take P rounded to one part there (the others do
   // again what they did).
   bool one_part[RT] = {}, again = false;
-  for (int c = c_begin; c < c_end;) {
+  while (left > 0) {
+    const Span span = item.span;
+    const int head = head_of(item), group0 = item.part / cv.heads * RT;   // first row tile
+    if (item.seq != q_seq || item.part != q_part) {
+      q_seq = item.seq;
+      q_part = item.part;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int row = (group0 + r) * 16 + col;
+        const int j = row / G;
+        t_row[r] = span.len - a.n_new + j;
+        // a row past the last takes the first's values, set to 0
+        const uint16_t* p = a.q + ((int64_t)item.seq * a.n_new + (row < rows ? j : 0)) * a.ldq +
+                            (int64_t)(head * G + (row < rows ? row % G : 0)) * hd;
+#pragma unroll
+        for (int k = 0; k < HB; ++k) {
+          const int d = k * 32 + grp * 8;
+          u32x4_t v = *(const u32x4_t*)(p + min(d, hd - 8));
+          if (row >= rows || d >= hd) v = u32x4_t{0, 0, 0, 0};
+          q[r][k] = __builtin_bit_cast(bf16x8_t, v);
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0x0f70);                  // vmcnt(0): nothing younger than V's loads in the loop
+    }
+    const int last_row = min(rows, (group0 + RT) * 16) - 1;
+    const int t_first = span.len - a.n_new + group0 * 16 / G, t_last = span.len - a.n_new + last_row / G;
+    const float z_scale = a.scale * (cv.k_scale != nullptr ? scalar_load(cv.k_scale + head) : 1.f) * kLog2e;
+    const float v_scale = cv.v_scale != nullptr ? scalar_load(cv.v_scale + head) : 1.f;
     float m[RT], l[RT];
     f32x4_t o[RT][DB];
 #pragma unroll
@@ -226,7 +284,7 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    while (cur.c == c) {
+    while (cur.after == left - 1) {
       const int k0 = cur.k0;
       const uint32_t seen_keys = valid;
       const bool whole = seen_keys == 0xffffffffu && k0 + kTile - 1 <= t_first &&
@@ -254,11 +312,11 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
         }
       // ask for the next tile's K, and the page of the one after it
       cur = ahead;
-      ahead = after(cur);
+      advance(ahead);
       valid = put_places(cur, page_ahead);
       page_ahead = ask_page(ahead);
       __builtin_amdgcn_sched_barrier(0);
-      ask_k();
+      ask_k(cur);
       __builtin_amdgcn_sched_barrier(0);
       bf16x8_t p_hi[RT], p_lo[RT];
 #pragma unroll
@@ -291,8 +349,10 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
           p_lo[r][i] = (__bf16)(p - (float)p_hi[r][i]);
         }
         l[r] = l[r] * shrink + sum;
+        if (__builtin_amdgcn_ballot_w64(shrink != 1.f) != 0) {   // (a maximum rose)
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[r][d] *= shrink;
+          for (int d = 0; d < DB; ++d) o[r][d] *= shrink;
+        }
       }
       // V into LDS, and transposed out of it
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -311,7 +371,7 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      ask_v();                                             // the next tile's
+      ask_v(cur);                                          // the next tile's
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
         // 16 lanes read 4 keys of 16 dimensions and get them by dimension
@@ -355,9 +415,8 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
       }
     }
 
-    // join the four waves: their sums into LDS as they are, weighed as they are added
-    bool odd = false;
     if (!again) {
+      bool odd = false;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         one_part[r] = false;
@@ -367,64 +426,41 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
           for (int i = 0; i < 4; ++i) one_part[r] = one_part[r] || !(fabsf(o[r][d][i]) < __builtin_inff());
         odd = odd || one_part[r];
       }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      l[r] = row_sum(l[r]);
-      if (grp == 0) {
-        stat[wave][r][col][0] = m[r];
-        stat[wave][r][col][1] = l[r];
+      if (__builtin_amdgcn_ballot_w64(odd) != 0) {
+        again = true;
+        prime();
+        continue;
       }
-    }
-    if (__syncthreads_or(odd)) {
-      again = true;
-      cur = first_from(c);
-      ahead = after(cur);
-      prime();
-      continue;
     }
     again = false;
-    float* ob = (float*)pool;                              // [wave][row][OS]
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      if ((group0 + r) * 16 >= rows) break;                // uniform
-      if ((group0 + r) * 16 + col < rows) {
+      const int row = (group0 + r) * 16 + col;
+      const float sum = row_sum(l[r]);
+      if (row >= rows) continue;
+      const int64_t qr = (int64_t)item.seq * a.n_new + row / G;
+      const int qh = head * G + row % G;
+      const int64_t at = qr * a.q_heads + qh;
+      if (span.n == 1) {
+        const float inv = sum == 0.f ? 0.f : v_scale / sum;
+        uint16_t* to = a.out + qr * a.ldo + (int64_t)qh * hd + grp * 4;
 #pragma unroll
-        for (int d = 0; d < DB; ++d) *(f32x4_t*)(ob + (wave * 16 + col) * OS + d * 16 + grp * 4) = o[r][d];
+        for (int d = 0; d < DB; ++d)
+          if (d * 16 < hd)
+            *(u32x2_t*)(to + d * 16) = u32x2_t{pack_bf16(o[r][d].x * inv, o[r][d].y * inv),
+                                               pack_bf16(o[r][d].z * inv, o[r][d].w * inv)};
+        if (grp == 0 && a.lse != nullptr) a.lse[at] = sum == 0.f ? kNegInf : m[r] * kLn2 + logf(sum);
+      } else {
+        const int64_t part_at = at * sp.max_chunks + item.c;
+        float* to = sp.sums + part_at * hd + grp * 4;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          if (d * 16 < hd) *(f32x4_t*)(to + d * 16) = o[r][d];
+        if (grp == 0) *(f32x2_t*)(sp.stats + part_at * 2) = f32x2_t{m[r], sum};
       }
-      __syncthreads();
-      const int n_rows = min(16, rows - (group0 + r) * 16);
-      for (int i = threadIdx.x; i < n_rows * (HP / 4); i += 256) {
-        const int row16 = i / (HP / 4), d = i % (HP / 4) * 4, row = (group0 + r) * 16 + row16;
-        if (d >= hd) continue;
-        float t = kNegInf, sum = 0.f;
-        for (int w = 0; w < 4; ++w) t = fmaxf(t, stat[w][r][row16][0]);
-        const float base = t == kNegInf ? 0.f : t;
-        f32x4_t s = {0.f, 0.f, 0.f, 0.f};
-        for (int w = 0; w < 4; ++w) {
-          const float f = exp2_fast(stat[w][r][row16][0] - base);
-          sum += f * stat[w][r][row16][1];
-          s += *(const f32x4_t*)(ob + (w * 16 + row16) * OS + d) * f;
-        }
-        const int64_t qr = (int64_t)seq * a.n_new + row / G;
-        const int qh = head * G + row % G;
-        const int64_t at = qr * a.q_heads + qh;
-        if (span.n == 1) {
-          const float inv = sum == 0.f ? 0.f : v_scale / sum;
-          uint16_t* to = a.out + qr * a.ldo + (int64_t)qh * hd + d;
-          *(u32x2_t*)to = u32x2_t{pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv)};
-          if (d == 0 && a.lse != nullptr) a.lse[at] = sum == 0.f ? kNegInf : t * kLn2 + logf(sum);
-        } else {
-          *(f32x4_t*)(sp.sums + (at * sp.max_chunks + c) * hd + d) = s;
-          if (d == 0) {
-            sp.stats[(at * sp.max_chunks + c) * 2] = t;
-            sp.stats[(at * sp.max_chunks + c) * 2 + 1] = sum;
-          }
-        }
-      }
-      __syncthreads();
     }
-    ++c;
+    --left;
+    next_item(item);
   }
 }
 
@@ -483,20 +519,28 @@ int64_t attention_workspace(int64_t seqs, int64_t capacity, int q_heads, int hd,
   return n == 1 ? 0 : seqs * n_new * q_heads * n * (hd + 2) * 4;
 }
 
-template <int HB, bool E4M3>
-static void attend(const AttendArgs& a, const Split& sp, int tiles, int grid, hipStream_t stream) {
-  if (tiles == 1)
-    cache_attention_kernel<HB, E4M3, 1><<<grid, 256, 0, stream>>>(a, sp);
-  else
-    cache_attention_kernel<HB, E4M3, 2><<<grid, 256, 0, stream>>>(a, sp);
+// As many workgroups as the chip holds at once (by their registers), if there is
+// a chunk for each wave: one that starts later starts its loads from nothing.
+template <int HB, bool E4M3, int RT>
+static void attend(const AttendArgs& a, const Split& sp, int64_t most, int cus, hipStream_t stream) {
+  constexpr int kHeld = HB * RT <= 2 ? 3 : HB * RT <= 4 ? 2 : 1;
+  const int grid = (int)std::min<int64_t>((most + 3) / 4, (int64_t)cus * kHeld);
+  cache_attention_kernel<HB, E4M3, RT><<<grid, 256, 0, stream>>>(a, sp);
 }
 
 template <int HB>
-static void attend_type(const AttendArgs& a, const Split& sp, int tiles, int grid, hipStream_t stream) {
-  if (a.cache.e4m3)
-    attend<HB, true>(a, sp, tiles, grid, stream);
-  else
-    attend<HB, false>(a, sp, tiles, grid, stream);
+static void attend_type(const AttendArgs& a, const Split& sp, int tiles, int64_t most, int cus, hipStream_t stream) {
+  if (a.cache.e4m3) {
+    if (tiles == 1)
+      attend<HB, true, 1>(a, sp, most, cus, stream);
+    else
+      attend<HB, true, 2>(a, sp, most, cus, stream);
+  } else {
+    if (tiles == 1)
+      attend<HB, false, 1>(a, sp, most, cus, stream);
+    else
+      attend<HB, false, 2>(a, sp, most, cus, stream);
+  }
 }
 
 hipError_t launch_cache_attention(const AttendArgs& args, int cus, void* workspace, hipStream_t stream) {
@@ -506,6 +550,7 @@ hipError_t launch_cache_attention(const AttendArgs& args, int cus, void* workspa
     cv.k = cv.v = (char*)const_cast<uint16_t*>(a.q);
     cv.head_bytes = 0;
   }
+  if (cv.pages_per_seq == 0) cv.table = a.lens;
   const int64_t capacity = (int64_t)cv.pages_per_seq << cv.page_shift;
   const int tiles = (a.q_heads / cv.heads * a.n_new + 15) / 16;
   Split sp;
@@ -514,18 +559,16 @@ hipError_t launch_cache_attention(const AttendArgs& args, int cus, void* workspa
   sp.sums = static_cast<float*>(workspace);
   sp.stats = sp.sums + heads * sp.max_chunks * cv.hd;
   sp.row_groups = (tiles + 1) / 2;
-  const int64_t pairs = (int64_t)cv.seqs * cv.heads * sp.row_groups;
-  sp.workers = (int)std::min<int64_t>(sp.max_chunks, std::max<int64_t>(1, (cus * 16 + pairs - 1) / pairs));
-  const int grid = (int)(pairs * sp.workers);
+  const int64_t most = (int64_t)cv.seqs * cv.heads * sp.row_groups * sp.max_chunks;
   switch ((cv.hd + 31) / 32) {
-    case 1: attend_type<1>(a, sp, tiles, grid, stream); break;
-    case 2: attend_type<2>(a, sp, tiles, grid, stream); break;
-    case 3: attend_type<3>(a, sp, tiles, grid, stream); break;
-    case 4: attend_type<4>(a, sp, tiles, grid, stream); break;
+    case 1: attend_type<1>(a, sp, tiles, most, cus, stream); break;
+    case 2: attend_type<2>(a, sp, tiles, most, cus, stream); break;
+    case 3: attend_type<3>(a, sp, tiles, most, cus, stream); break;
+    case 4: attend_type<4>(a, sp, tiles, most, cus, stream); break;
     case 5:
-    case 6: attend_type<6>(a, sp, tiles, grid, stream); break;
+    case 6: attend_type<6>(a, sp, tiles, most, cus, stream); break;
     case 7:
-    case 8: attend_type<8>(a, sp, tiles, grid, stream); break;
+    case 8: attend_type<8>(a, sp, tiles, most, cus, stream); break;
     default: return hipErrorInvalidValue;
   }
   hipError_t e = hipGetLastError();

@@ -64,7 +64,7 @@ __host__ __device__ inline int64_t token_bytes_at(const CacheView& c, int32_t pa
 // the sequence's own length (and the window), so that a row's bits do not
 // depend on the batch.
 constexpr int kTile = 32;            // keys a wave takes at a time
-constexpr int kBlock = 256;          // keys whose places are looked up together
+constexpr int kLeastChunk = 128;     // keys
 constexpr int kMaxChunks = 128;      // of one sequence
 
 struct Span {
@@ -78,9 +78,9 @@ __host__ __device__ inline Span span_of(int len, int n_new, int window) {
   s.first = lo > 0 ? (int)lo : 0;
   s.start = s.first & ~(kTile - 1);
   const int keys = len > s.start ? len - s.start : 0;
-  const int blocks = (keys + kBlock - 1) / kBlock;
-  s.chunk = kBlock * ((blocks + kMaxChunks - 1) / kMaxChunks);
-  if (s.chunk == 0) s.chunk = kBlock;
+  const int least = (keys + kLeastChunk - 1) / kLeastChunk;
+  s.chunk = kLeastChunk * ((least + kMaxChunks - 1) / kMaxChunks);
+  if (s.chunk == 0) s.chunk = kLeastChunk;
   s.n = (keys + s.chunk - 1) / s.chunk;
   if (s.n == 0) s.n = 1;             // no keys: one empty chunk writes the zeros
   return s;
@@ -93,7 +93,7 @@ inline int most_chunks(int64_t capacity, int n_new, int window) {
     const int64_t seen = (int64_t)window + n_new - 1 + kTile - 1;
     keys = keys < seen ? keys : seen;
   }
-  const int64_t n = (keys + kBlock - 1) / kBlock;
+  const int64_t n = (keys + kLeastChunk - 1) / kLeastChunk;
   return n < 1 ? 1 : n > kMaxChunks ? kMaxChunks : (int)n;
 }
 

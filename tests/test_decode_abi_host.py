@@ -198,8 +198,10 @@ def test_workspace_sizes_refuse_what_the_calls_refuse(L):
         ctypes.addressof(B.KvCacheDesc(**{**CACHE, **over})), *a)
     assert size(4, 1, 0) == 0 and size(3, 1, 0) == S and size(4, 0, 0) == S and size(4, 1, -1) == G
     assert size(4, 1, 0, page_size=3) == S and L.ds_cache_attention_rows_workspace(None, 4, 1, 0) == N
-    assert size(4, 1, 0, pages_per_seq=17) == 3 * 4 * 2 * 66 * 4                # two chunks of 256
-    assert size(4, 1, 100, pages_per_seq=1000) == 0                             # a window within one
+    assert size(4, 1, 0, pages_per_seq=8) == 0                                  # one chunk of 128: nothing to join
+    assert size(4, 1, 0, pages_per_seq=17) == 3 * 4 * 3 * 66 * 4                # three
+    assert size(4, 1, 97, pages_per_seq=1000) == 0                              # a window within one
+    assert size(4, 1, 98, pages_per_seq=1000) == 3 * 4 * 2 * 66 * 4
     assert size(4, 1, 0, pages_per_seq=1 << 25) == size(4, 1, 0, pages_per_seq=1 << 11)   # 128 chunks at most
     assert size(4, 1, 0, n_seqs=1 << 21) == 0 and size(4, 1, 0, n_seqs=(1 << 21) + 1) == S
     del cache

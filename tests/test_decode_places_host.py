@@ -71,7 +71,7 @@ int main() {
           const Span s = span_of(len, n_new, window);
           const int64_t first = window ? (int64_t)len - n_new - window + 1 : 0;
           NEED(s.first == (first > 0 ? first : 0) && s.start % kTile == 0 && s.start <= s.first);
-          NEED(s.first - s.start < kTile && s.chunk % kBlock == 0 && s.chunk > 0);
+          NEED(s.first - s.start < kTile && s.chunk % kLeastChunk == 0 && s.chunk > 0);
           NEED(s.n >= 1 && s.n <= kMaxChunks && s.n <= most_chunks(cap, n_new, window));
           NEED((int64_t)s.start + (int64_t)s.n * s.chunk >= len);
           NEED(s.n == 1 || (int64_t)s.start + (int64_t)(s.n - 1) * s.chunk < len);   // none empty
