@@ -122,18 +122,19 @@ __device__ __forceinline__ Item item_at(const AttendArgs& a, int parts, int64_t 
 
 // HB: head_dim in blocks of 32, rounded up.  RT: tiles of 16 rows a wave.
 //
-// A wave walks the tiles of 32 keys of its chunks, one ahead with its loads: the
-// next tile's K is asked for as soon as this one's has gone into S, its V as soon
-// as this one's is in LDS, the page of the one after before either.  No wave
-// waits for another.
+// A wave walks its chunks by blocks of 128 keys, whose places it looks up
+// together, a block ahead, and those by tiles of 32, a tile ahead with their
+// loads: the next tile's K is asked for as soon as this one's has gone into S,
+// its V as soon as this one's is in LDS.  No wave waits for another.
 template <int HB, bool E4M3, int RT>
 __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_kernel(const AttendArgs a,
                                                                                     const Split sp) {
   constexpr int HP = HB * 32, DB = HB * 2;                 // padded head_dim; its blocks of 16
   constexpr int VS = HP + 16;                              // bf16 a row of V in LDS: rows start 8 banks apart
   constexpr int VP = E4M3 ? HB : 2 * HB, PPR = E4M3 ? 2 * HB : 4 * HB;   // V's 16-byte pieces a lane, a row
+  constexpr int EB = E4M3 ? 1 : 2;                         // bytes an element
   __shared__ __attribute__((aligned(16))) uint16_t v_tiles[4][kTile * VS];
-  __shared__ int64_t places[4][kTile];                     // byte offset of a key's token
+  __shared__ int64_t places[4][2][kLeastChunk];            // byte offset of a key's token
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const CacheView& cv = a.cache;
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
   int left = (int)(list_hi - list_lo);                     // items still to do, this one too
 
   auto chunk_lo = [](const Item& t) { return t.span.start + t.c * t.span.chunk; };
+  auto chunk_hi = [&](const Item& t) { return min(t.span.len, chunk_lo(t) + t.span.chunk); };
   auto next_item = [&](Item& t) {
     if (++t.c < t.span.n) return;
     t.c = 0;
@@ -156,85 +158,86 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
     ++t.seq;
     if (t.seq < cv.seqs) t.span = span_here(a, t.seq);
   };
-  // A tile: the item it is in, how many items come after that one
-  // (-1: there is no such tile), its first key.
-  struct Tile {
-    Item it;
-    int after, k0;
-  };
-  auto settle = [&](Tile& t) {                             // on to the next item that has a tile
-    while (t.after >= 0 && t.k0 >= min(t.it.span.len, chunk_lo(t.it) + t.it.span.chunk)) {
-      if (--t.after < 0) break;
-      next_item(t.it);
-      t.k0 = chunk_lo(t.it);
+  // The block that comes after the one at work: its item, how many items come
+  // after that (-1: there is no such block), its first key.
+  Item soon;
+  int soon_after, soon_k0;
+  auto soon_from = [&]() {                                 // on to an item that has keys
+    while (soon_after >= 0 && soon_k0 >= chunk_hi(soon)) {
+      if (--soon_after < 0) break;
+      next_item(soon);
+      soon_k0 = chunk_lo(soon);
     }
   };
-  auto advance = [&](Tile& t) {
-    t.k0 += kTile;
-    settle(t);
+  // the pages of its keys: this lane's and the 64th after it (of the last key past it)
+  int32_t pages[2];
+  auto ask_pages = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = min(soon_k0 + i * 64 + lane, soon.span.len - 1);
+      pages[i] = cv.table[soon_after >= 0 ? table_entry(cv, soon.seq, key) : 0];
+    }
   };
-  // the page of this lane's key (lanes 0..31; of the last key past it)
-  auto ask_page = [&](const Tile& t) {
-    const int key = min(t.k0 + (lane & 31), t.it.span.len - 1);
-    return cv.table[t.after >= 0 ? table_entry(cv, t.it.seq, key) : 0];
+  uint64_t valid[2], soon_valid[2];                        // which keys are in the cache and seen
+  int64_t soon_head = 0;                                   // the byte offset of its head
+  auto put_places = [&](int64_t* to) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = soon_k0 + i * 64 + lane;
+      const int64_t at = soon_after >= 0 && key >= soon.span.first && key < soon.span.len
+                             ? token_bytes_at(cv, pages[i], key) : -1;
+      to[i * 64 + lane] = at < 0 ? 0 : at;
+      soon_valid[i] = __builtin_amdgcn_ballot_w64(at >= 0);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    soon_head = soon_after >= 0 ? (soon.part % cv.heads) * cv.head_bytes : 0;
   };
   typedef std::conditional_t<E4M3, u32x2_t, u32x4_t> kword_t;   // eight values
   kword_t kw[2][HB];                                       // a tile on its way
   u32x4_t vw[VP];
-  uint32_t valid = 0;                                      // which of its keys are in the cache and seen
   uint16_t* vt = v_tiles[wave];
-  int64_t* place = places[wave];
-  auto put_places = [&](const Tile& t, int32_t page) {
-    const int key = t.k0 + (lane & 31);
-    const int64_t at =
-        t.after >= 0 && key >= t.it.span.first && key < t.it.span.len ? token_bytes_at(cv, page, key) : -1;
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    if (lane < 32) place[lane] = at < 0 ? 0 : at;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    return (uint32_t)__builtin_amdgcn_ballot_w64(at >= 0);
-  };
-  auto head_of = [&](const Item& t) { return t.part < parts ? t.part % cv.heads : 0; };
   // Every lane loads, one without a key of its own the cache's first token (and
-  // the first dimensions in place of those past the head): a load under a
-  // condition is waited for at once.  What no row sees is masked where it is used.
-  const int past_k = hd - 8;
-  auto ask_k = [&](const Tile& t) {                        // lane (col, grp): key col, dims 8 grp.. of each 32
-    const char* base = cv.k + head_of(t.it) * cv.head_bytes;
+  // dimensions of the head in place of those past it): a load under a condition
+  // is waited for at once.  What no row sees is masked where it is used.
+  int k_off[2];                                            // the last two blocks of 32 dimensions
+#pragma unroll
+  for (int i = 0; i < 2; ++i) k_off[i] = min((HB - 2 + i) * 32 + grp * 8, hd - 8) * EB;
+  auto ask_k = [&](int64_t head, const int64_t* at) {      // lane (col, grp): key col, dims 8 grp.. of each 32
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const char* at = base + place[half * 16 + col];
+      const char* p = cv.k + (head + at[half * 16 + col]);
 #pragma unroll
       for (int k = 0; k < HB; ++k) {
-        const int d = min(k * 32 + grp * 8, past_k);
-        kw[half][k] = *(const kword_t*)(at + d * (E4M3 ? 1 : 2));
+        if (k >= HB - 2)
+          kw[half][k] = *(const kword_t*)(p + k_off[k - HB + 2]);
+        else
+          kw[half][k] = *(const kword_t*)(p + grp * 8 * EB + k * 32 * EB);
       }
     }
   };
-  auto ask_v = [&](const Tile& t) {                        // 16 bytes at a time, rows side by side
-    const char* base = cv.v + head_of(t.it) * cv.head_bytes;
+  auto ask_v = [&](int64_t head, const int64_t* at) {      // 16 bytes at a time, rows side by side
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
-      const int piece = i * 64 + lane, d = piece % PPR * (E4M3 ? 16 : 8);
-      vw[i] = *(const u32x4_t*)(base + place[piece / PPR] + min(d, hd - (E4M3 ? 16 : 8)) * (E4M3 ? 1 : 2));
+      const int piece = i * 64 + lane, d = min(piece % PPR * (16 / EB), hd - 16 / EB);
+      vw[i] = *(const u32x4_t*)(cv.v + (head + at[piece / PPR]) + d * EB);
     }
   };
-  Tile cur, ahead;
-  int32_t page_ahead;
-  auto prime = [&]() {                                     // from `item` on: the loads of `cur`, the page of `ahead`
-    cur = Tile{item, left - 1, chunk_lo(item)};
-    settle(cur);
-    ahead = cur;
-    advance(ahead);
-    const int32_t page = ask_page(cur);
-    page_ahead = ask_page(ahead);
-    valid = put_places(cur, page);
+  int buf = 0;                                             // which places are the block's at work
+  auto prime = [&]() {                                     // from `item` on
+    soon = item;
+    soon_after = left - 1;
+    soon_k0 = chunk_lo(item);
+    soon_from();
+    ask_pages();
+    put_places(places[wave][buf]);
     // K's loads before V's, as in the loop, and on every way into it: how many
     // younger loads a tile may leave on their way there is the least of them all
     __builtin_amdgcn_sched_barrier(0);
-    ask_k(cur);
+    ask_k(soon_head, places[wave][buf]);
     __builtin_amdgcn_sched_barrier(0);
-    ask_v(cur);
+    ask_v(soon_head, places[wave][buf]);
     __builtin_amdgcn_sched_barrier(0);
   };
   prime();
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
   bool one_part[RT] = {}, again = false;
   while (left > 0) {
     const Span span = item.span;
-    const int head = head_of(item), group0 = item.part / cv.heads * RT;   // first row tile
+    const int head = item.part % cv.heads, group0 = item.part / cv.heads * RT;   // first row tile
     if (item.seq != q_seq || item.part != q_part) {
       q_seq = item.seq;
       q_part = item.part;
@@ -274,7 +277,6 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
     const int last_row = min(rows, (group0 + RT) * 16) - 1;
     const int t_first = span.len - a.n_new + group0 * 16 / G, t_last = span.len - a.n_new + last_row / G;
     const float z_scale = a.scale * (cv.k_scale != nullptr ? scalar_load(cv.k_scale + head) : 1.f) * kLog2e;
-    const float v_scale = cv.v_scale != nullptr ? scalar_load(cv.v_scale + head) : 1.f;
     float m[RT], l[RT];
     f32x4_t o[RT][DB];
 #pragma unroll
@@ -284,135 +286,181 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    while (cur.after == left - 1) {
-      const int k0 = cur.k0;
-      const uint32_t seen_keys = valid;
-      const bool whole = seen_keys == 0xffffffffu && k0 + kTile - 1 <= t_first &&
-                         (a.window == 0 || k0 > t_last - a.window);
-      f32x4_t z[RT][2];
+    const int hi = chunk_hi(item);
+    for (int kb = chunk_lo(item); kb < hi; kb += kLeastChunk) {
+      valid[0] = soon_valid[0];
+      valid[1] = soon_valid[1];
+      const int64_t block_head = soon_head;
+      soon_k0 += kLeastChunk;
+      soon_from();
+      ask_pages();
+      const int tiles = (min(hi - kb, kLeastChunk) + kTile - 1) / kTile;
+      for (int tile = 0; tile < tiles; ++tile) {
+        const int k0 = kb + tile * kTile;
+        const uint32_t keys = (uint32_t)((tile < 2 ? valid[0] : valid[1]) >> (tile % 2 * 32));
+        // every row sees every key; some rows see a key that others do not
+        const bool whole = keys == 0xffffffffu && k0 + kTile - 1 <= t_first &&
+                           (a.window == 0 || k0 > t_last - a.window);
+        const bool mixed = t_first < t_last &&
+                           (k0 + kTile - 1 > t_first || (a.window != 0 && k0 <= t_last - a.window));
+        f32x4_t z[RT][2];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) z[r][0] = z[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < RT; ++r) z[r][0] = z[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < HB; ++k)
+        for (int k = 0; k < HB; ++k)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          u32x4_t w;
-          if constexpr (E4M3) {
-            const u32x2_t a0 = widen4(kw[half][k].x), a1 = widen4(kw[half][k].y);
-            w = u32x4_t{a0.x, a0.y, a1.x, a1.y};
-          } else {
-            w = kw[half][k];
+          for (int half = 0; half < 2; ++half) {
+            u32x4_t w;
+            if constexpr (E4M3) {
+              const u32x2_t a0 = widen4(kw[half][k].x), a1 = widen4(kw[half][k].y);
+              w = u32x4_t{a0.x, a0.y, a1.x, a1.y};
+            } else {
+              w = kw[half][k];
+            }
+            if (k >= HB - 2)                               // dimensions past the head: 0, as q is
+              if (k * 32 + grp * 8 >= hd) w = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              z[r][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), q[r][k],
+                                                                   z[r][half], 0, 0, 0);
           }
-          if (k == HB - 1 || k == HB - 2)                  // dimensions past the head: 0, as q is
-            if (k * 32 + grp * 8 >= hd) w = u32x4_t{0, 0, 0, 0};
+        // the next tile, of this block or of the one after it
+        if (tile == tiles - 1) put_places(places[wave][buf ^ 1]);
+        const int64_t* next = tile == tiles - 1 ? places[wave][buf ^ 1] : places[wave][buf] + (tile + 1) * kTile;
+        const int64_t next_head = tile == tiles - 1 ? soon_head : block_head;
+        __builtin_amdgcn_sched_barrier(0);
+        ask_k(next_head, next);
+        __builtin_amdgcn_sched_barrier(0);
+        bf16x8_t p_hi[RT], p_lo[RT];
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
-            z[r][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w), q[r][k],
-                                                                 z[r][half], 0, 0, 0);
-        }
-      // ask for the next tile's K, and the page of the one after it
-      cur = ahead;
-      advance(ahead);
-      valid = put_places(cur, page_ahead);
-      page_ahead = ask_page(ahead);
-      __builtin_amdgcn_sched_barrier(0);
-      ask_k(cur);
-      __builtin_amdgcn_sched_barrier(0);
-      bf16x8_t p_hi[RT], p_lo[RT];
+        for (int r = 0; r < RT; ++r) {
+          float zs[8];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float zs[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) zs[i] = z[r][i / 4][i % 4] * z_scale;
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int b = i / 4 * 16 + grp * 4 + i % 4, key = k0 + b;
-            const bool seen = ((seen_keys >> b) & 1u) != 0 && key <= t_row[r] &&
-                              (a.window == 0 || key > t_row[r] - a.window);
-            zs[i] = seen ? zs[i] : kNegInf;
-          }
-        }
-        float top = zs[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, zs[i]);
-        const float m_new = fmaxf(m[r], row_max(top));
-        const float base = m_new == kNegInf ? 0.f : m_new;
-        const float shrink = exp2_fast(m[r] - base);
-        m[r] = m_new;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = exp2_fast(zs[i] - base);
-          sum += p;
-          p_hi[r][i] = (__bf16)p;
-          p_lo[r][i] = (__bf16)(p - (float)p_hi[r][i]);
-        }
-        l[r] = l[r] * shrink + sum;
-        if (__builtin_amdgcn_ballot_w64(shrink != 1.f) != 0) {   // (a maximum rose)
-#pragma unroll
-          for (int d = 0; d < DB; ++d) o[r][d] *= shrink;
-        }
-      }
-      // V into LDS, and transposed out of it
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        const int piece = i * 64 + lane;
-        uint16_t* to = vt + piece / PPR * VS + piece % PPR * (E4M3 ? 16 : 8);
-        if constexpr (E4M3) {
-          const u32x2_t a0 = widen4(vw[i].x), a1 = widen4(vw[i].y), a2 = widen4(vw[i].z), a3 = widen4(vw[i].w);
-          ((u32x4_t*)to)[0] = u32x4_t{a0.x, a0.y, a1.x, a1.y};
-          ((u32x4_t*)to)[1] = u32x4_t{a2.x, a2.y, a3.x, a3.y};
-        } else {
-          *(u32x4_t*)to = vw[i];
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      ask_v(cur);                                          // the next tile's
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        // 16 lanes read 4 keys of 16 dimensions and get them by dimension
-        typedef short s16x8_t __attribute__((ext_vector_type(8)));
-        typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
-        const uint16_t* from = vt + (grp * 4 + col / 4) * VS + d * 16 + col % 4 * 4;
-        const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)from);
-        const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(from + 16 * VS));
-        const s16x8_t x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-        if (whole) {
-          const bf16x8_t v = __builtin_bit_cast(bf16x8_t, x);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_hi[r], o[r][d], 0, 0, 0);
-            const f32x4_t s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_lo[r], o[r][d], 0, 0, 0);
-            o[r][d] = again && one_part[r] ? o[r][d] : s;
-          }
-        } else {
-          // a key that a row does not see must not reach it even as 0 times an
-          // infinity: each new token's rows get V with its own keys
-          f32x4_t was[RT];
-#pragma unroll
-          for (int r = 0; r < RT; ++r) was[r] = o[r][d];
-          for (int t = t_first; t <= t_last; ++t) {
-            s16x8_t y;
+          for (int i = 0; i < 8; ++i) zs[i] = z[r][i / 4][i % 4] * z_scale;
+          if (!whole) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int b = i / 4 * 16 + grp * 4 + i % 4, key = k0 + b;
-              const bool seen = ((seen_keys >> b) & 1u) != 0 && key <= t && (a.window == 0 || key > t - a.window);
-              y[i] = seen ? x[i] : (short)0;
+              const bool seen = ((keys >> b) & 1u) != 0 && key <= t_row[r] &&
+                                (a.window == 0 || key > t_row[r] - a.window);
+              zs[i] = seen ? zs[i] : kNegInf;
             }
-            const bf16x8_t v = __builtin_bit_cast(bf16x8_t, y);
+          }
+          float top = zs[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) top = fmaxf(top, zs[i]);
+          const float m_new = fmaxf(m[r], row_max(top));
+          const float base = m_new == kNegInf ? 0.f : m_new;
+          const float shrink = exp2_fast(m[r] - base);
+          m[r] = m_new;
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float p = exp2_fast(zs[i] - base);
+            sum += p;
+            p_hi[r][i] = (__bf16)p;
+            p_lo[r][i] = (__bf16)(p - (float)p_hi[r][i]);
+          }
+          l[r] = l[r] * shrink + sum;
+          if (__builtin_amdgcn_ballot_w64(shrink != 1.f) != 0) {   // (a maximum rose)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[r][d] *= shrink;
+          }
+        }
+        // V into LDS, keys that are not in `mask` as zeros
+        auto put_v = [&](uint32_t mask) {
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int i = 0; i < VP; ++i) {
+            const int piece = i * 64 + lane;
+            uint16_t* to = vt + piece / PPR * VS + piece % PPR * (16 / EB);
+            u32x4_t w = vw[i];
+            if (mask != 0xffffffffu)
+              if (((mask >> (piece / PPR)) & 1u) == 0) w = u32x4_t{0, 0, 0, 0};
+            if constexpr (E4M3) {
+              const u32x2_t a0 = widen4(w.x), a1 = widen4(w.y), a2 = widen4(w.z), a3 = widen4(w.w);
+              ((u32x4_t*)to)[0] = u32x4_t{a0.x, a0.y, a1.x, a1.y};
+              ((u32x4_t*)to)[1] = u32x4_t{a2.x, a2.y, a3.x, a3.y};
+            } else {
+              *(u32x4_t*)to = w;
+            }
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+        };
+        // and transposed out of it: 16 lanes read 4 keys of 16 dimensions and get
+        // them by dimension
+        auto get_v = [&](int d) {
+          typedef short s16x8_t __attribute__((ext_vector_type(8)));
+          typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+          const uint16_t* from = vt + (grp * 4 + col / 4) * VS + d * 16 + col % 4 * 4;
+          const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)from);
+          const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(from + 16 * VS));
+          const s16x8_t x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+          return __builtin_bit_cast(bf16x8_t, x);
+        };
+        // A key that a row does not see must not reach it even as 0 times an
+        // infinity.  Where no row sees it, it is a zero; where some do, and it does
+        // hold one, each new token's rows get V with that token's keys.
+        bool apart = false;
+        if (mixed) {
+          const int seen_by_all = t_first, from = a.window != 0 ? t_last - a.window : -1;
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < VP; ++i) {
+            const int b = (i * 64 + lane) / PPR, key = k0 + b;
+            const bool some = ((keys >> b) & 1u) != 0 && (key > seen_by_all || key <= from);
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if constexpr (E4M3) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) bad = bad || ((vw[i][j] >> k) & 0x7fu) == 0x7fu;
+              } else {
+                bad = bad || (vw[i][j] & 0x7f80u) == 0x7f80u || (vw[i][j] & 0x7f800000u) == 0x7f800000u;
+              }
+            odd = odd || (some && bad);
+          }
+          apart = __builtin_amdgcn_ballot_w64(odd) != 0;
+        }
+        if (apart) {
+          for (int t = t_first; t <= t_last; ++t) {
+            uint32_t mask = 0;
+            for (int b = 0; b < kTile; ++b)
+              if (k0 + b <= t && (a.window == 0 || k0 + b > t - a.window)) mask |= 1u << b;
+            put_v(keys & mask);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              const bf16x8_t v = get_v(d);
+#pragma unroll
+              for (int r = 0; r < RT; ++r) {
+                const f32x4_t h = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_hi[r], o[r][d], 0, 0, 0);
+                const f32x4_t s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_lo[r], h, 0, 0, 0);
+                if (t_row[r] == t) o[r][d] = again && one_part[r] ? h : s;
+              }
+            }
+          }
+        } else {
+          put_v(keys);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        ask_v(next_head, next);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!apart) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d) {
+            const bf16x8_t v = get_v(d);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-              const f32x4_t h = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_hi[r], was[r], 0, 0, 0);
-              const f32x4_t s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_lo[r], h, 0, 0, 0);
-              if (t_row[r] == t) o[r][d] = again && one_part[r] ? h : s;
+              o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_hi[r], o[r][d], 0, 0, 0);
+              const f32x4_t s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_lo[r], o[r][d], 0, 0, 0);
+              o[r][d] = again && one_part[r] ? o[r][d] : s;
             }
           }
         }
       }
+      buf ^= 1;
     }
 
     if (!again) {
@@ -433,6 +481,7 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
       }
     }
     again = false;
+    const float v_scale = cv.v_scale != nullptr ? scalar_load(cv.v_scale + head) : 1.f;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const int row = (group0 + r) * 16 + col;
