@@ -1,8 +1,8 @@
 // Attention of each sequence's newest tokens over the paged cache.
 //
 //   z_u = scale <q, K_u>,  lse = log sum exp z_u,  out = sum exp(z_u - lse) V_u
-// over the tokens u that a row sees, in one pass: with m the largest z so far,
-// l = sum exp(z - m) and O = sum exp(z - m) V are rescaled when m rises.
+// over the tokens u that a row sees, in one pass: with m about the largest
+// z so far, l = sum exp(z - m) and O = sum exp(z - m) V are rescaled when m rises.
 //
 // The n new tokens of a sequence and the G = q heads / kv heads that share a
 // kv head make n G rows over the same keys and values, 16 of them a tile of
@@ -26,6 +26,7 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kRise = 8.f;         // of z log2 e
 
 struct Split {
   float* sums;                       // [row][head][max_chunks][hd]
@@ -118,6 +119,62 @@ __device__ __forceinline__ Item item_at(const AttendArgs& a, int parts, int64_t 
   it.part = rest / it.span.n;
   it.c = rest % it.span.n;
   return it;
+}
+
+// O of one row's head over one chunk, key by key in fp32 (the wave's lanes share
+// its dimensions), from its m and l: what the matrix instructions cannot keep
+// apart is handed here.
+template <bool E4M3>
+__device__ __forceinline__ void plain_row(const AttendArgs& a, const Split& sp, const Item& item, int head, int row,
+                                          float m, float l, float z_scale, float v_scale, int lane) {
+  const CacheView& cv = a.cache;
+  const int hd = cv.hd, G = a.q_heads / cv.heads;
+  const int64_t qr = (int64_t)item.seq * a.n_new + row / G;
+  const int qh = head * G + row % G;
+  const int t = item.span.len - a.n_new + row / G;
+  int lo = item.span.start + item.c * item.span.chunk;
+  const int hi = min(min(item.span.len, lo + item.span.chunk), t + 1);
+  lo = max(lo, item.span.first);
+  if (a.window != 0) lo = max(lo, t - a.window + 1);
+  auto value = [&](const char* p, int d) {
+    if constexpr (E4M3)
+      return __builtin_amdgcn_cvt_f32_fp8(*(const uint8_t*)(p + d), 0);
+    else
+      return bf_lo(*(const uint16_t*)(p + d * 2));
+  };
+  const float base = m == kNegInf ? 0.f : m;
+  float q[4], o[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int d = i * 64 + lane;
+    q[i] = d < hd ? bf_lo(a.q[qr * a.ldq + (int64_t)qh * hd + d]) : 0.f;
+  }
+  for (int key = lo; key < hi; ++key) {
+    const int64_t at = token_bytes_at(cv, cv.table[table_entry(cv, item.seq, key)], key);
+    if (at < 0) continue;
+    const char* k = cv.k + head * cv.head_bytes + at;
+    const char* v = cv.v + head * cv.head_bytes + at;
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i * 64 + lane < hd) z = __builtin_fmaf(q[i], value(k, i * 64 + lane), z);
+    z = wave_sum(z) * z_scale;
+    if (z == kNegInf) continue;                            // masked
+    const float p = exp2_fast(z - base);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i * 64 + lane < hd) o[i] += p * value(v, i * 64 + lane);
+  }
+  const int64_t part_at = (qr * a.q_heads + qh) * sp.max_chunks + item.c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int d = i * 64 + lane;
+    if (d >= hd) continue;
+    if (item.span.n == 1)
+      a.out[qr * a.ldo + (int64_t)qh * hd + d] = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[i] / l * v_scale, 0.f);
+    else
+      sp.sums[part_at * hd + d] = o[i];
+  }
 }
 
 // HB: head_dim in blocks of 32, rounded up.  RT: tiles of 16 rows a wave.
@@ -245,11 +302,6 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
   int t_row[RT];                                           // this lane's row of each row tile: its token
   bf16x8_t q[RT][HB];                                      // and its q, as the matrix operand
   int q_seq = -1, q_part = -1;
-  // A second pass over a chunk is for sums that came out infinite or NaN: where V
-  // holds an infinity, its products with the two parts of a P may cancel to NaN,
-  // so the lanes with such sums take P rounded to one part there (the others do
-  // again what they did).
-  bool one_part[RT] = {}, again = false;
   while (left > 0) {
     const Span span = item.span;
     const int head = item.part % cv.heads, group0 = item.part / cv.heads * RT;   // first row tile
@@ -279,10 +331,12 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
     const float z_scale = a.scale * (cv.k_scale != nullptr ? scalar_load(cv.k_scale + head) : 1.f) * kLog2e;
     float m[RT], l[RT];
     f32x4_t o[RT][DB];
+    bool odd[RT];                                          // this row is to be summed by itself, below
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       m[r] = kNegInf;
       l[r] = 0.f;
+      odd[r] = false;
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
@@ -349,7 +403,10 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
           float top = zs[0];
 #pragma unroll
           for (int i = 1; i < 8; ++i) top = fmaxf(top, zs[i]);
-          const float m_new = fmaxf(m[r], row_max(top));
+          // m follows the largest z only where that is kRise above it: sums stay
+          // within 2^kRise of the largest weight, and are rescaled seldom
+          top = row_max(top);
+          const float m_new = top > m[r] + kRise ? top : m[r];
           const float base = m_new == kNegInf ? 0.f : m_new;
           const float shrink = exp2_fast(m[r] - base);
           m[r] = m_new;
@@ -362,55 +419,20 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
             p_lo[r][i] = (__bf16)(p - (float)p_hi[r][i]);
           }
           l[r] = l[r] * shrink + sum;
-          if (__builtin_amdgcn_ballot_w64(shrink != 1.f) != 0) {   // (a maximum rose)
+          if (__builtin_amdgcn_ballot_w64(shrink != 1.f) != 0) {
 #pragma unroll
             for (int d = 0; d < DB; ++d) o[r][d] *= shrink;
           }
         }
-        // V into LDS, keys that are not in `mask` as zeros
-        auto put_v = [&](uint32_t mask) {
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-          __builtin_amdgcn_wave_barrier();
-#pragma unroll
-          for (int i = 0; i < VP; ++i) {
-            const int piece = i * 64 + lane;
-            uint16_t* to = vt + piece / PPR * VS + piece % PPR * (16 / EB);
-            u32x4_t w = vw[i];
-            if (mask != 0xffffffffu)
-              if (((mask >> (piece / PPR)) & 1u) == 0) w = u32x4_t{0, 0, 0, 0};
-            if constexpr (E4M3) {
-              const u32x2_t a0 = widen4(w.x), a1 = widen4(w.y), a2 = widen4(w.z), a3 = widen4(w.w);
-              ((u32x4_t*)to)[0] = u32x4_t{a0.x, a0.y, a1.x, a1.y};
-              ((u32x4_t*)to)[1] = u32x4_t{a2.x, a2.y, a3.x, a3.y};
-            } else {
-              *(u32x4_t*)to = w;
-            }
-          }
-          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-          __builtin_amdgcn_wave_barrier();
-        };
-        // and transposed out of it: 16 lanes read 4 keys of 16 dimensions and get
-        // them by dimension
-        auto get_v = [&](int d) {
-          typedef short s16x8_t __attribute__((ext_vector_type(8)));
-          typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
-          const uint16_t* from = vt + (grp * 4 + col / 4) * VS + d * 16 + col % 4 * 4;
-          const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)from);
-          const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(from + 16 * VS));
-          const s16x8_t x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-          return __builtin_bit_cast(bf16x8_t, x);
-        };
         // A key that a row does not see must not reach it even as 0 times an
-        // infinity.  Where no row sees it, it is a zero; where some do, and it does
-        // hold one, each new token's rows get V with that token's keys.
-        bool apart = false;
+        // infinity.  A key that no row sees is made zeros; one that some see, and
+        // that holds infinities or NaN, too, and those rows are summed by themselves.
         if (mixed) {
-          const int seen_by_all = t_first, from = a.window != 0 ? t_last - a.window : -1;
-          bool odd = false;
+          const int from = a.window != 0 ? t_last - a.window : -1;
+          uint32_t bad_keys = 0;
 #pragma unroll
           for (int i = 0; i < VP; ++i) {
             const int b = (i * 64 + lane) / PPR, key = k0 + b;
-            const bool some = ((keys >> b) & 1u) != 0 && (key > seen_by_all || key <= from);
             bool bad = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -420,94 +442,110 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
               } else {
                 bad = bad || (vw[i][j] & 0x7f80u) == 0x7f80u || (vw[i][j] & 0x7f800000u) == 0x7f800000u;
               }
-            odd = odd || (some && bad);
-          }
-          apart = __builtin_amdgcn_ballot_w64(odd) != 0;
-        }
-        if (apart) {
-          for (int t = t_first; t <= t_last; ++t) {
-            uint32_t mask = 0;
-            for (int b = 0; b < kTile; ++b)
-              if (k0 + b <= t && (a.window == 0 || k0 + b > t - a.window)) mask |= 1u << b;
-            put_v(keys & mask);
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-              const bf16x8_t v = get_v(d);
-#pragma unroll
-              for (int r = 0; r < RT; ++r) {
-                const f32x4_t h = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_hi[r], o[r][d], 0, 0, 0);
-                const f32x4_t s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_lo[r], h, 0, 0, 0);
-                if (t_row[r] == t) o[r][d] = again && one_part[r] ? h : s;
-              }
+            if (bad && ((keys >> b) & 1u) != 0 && (key > t_first || key <= from)) {
+              vw[i] = u32x4_t{0, 0, 0, 0};
+              bad_keys |= 1u << b;
             }
           }
-        } else {
-          put_v(keys);
+          if (__builtin_amdgcn_ballot_w64(bad_keys != 0) != 0) {
+#pragma unroll
+            for (int i = 32; i > 0; i >>= 1) bad_keys |= __shfl_xor(bad_keys, i);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              for (int b = 0; b < kTile; ++b)
+                odd[r] = odd[r] || (((bad_keys >> b) & 1u) != 0 && k0 + b <= t_row[r] &&
+                                    (a.window == 0 || k0 + b > t_row[r] - a.window));
+          }
         }
+        // V into LDS
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+          const int piece = i * 64 + lane;
+          uint16_t* to = vt + piece / PPR * VS + piece % PPR * (16 / EB);
+          u32x4_t w = vw[i];
+          if (keys != 0xffffffffu)
+            if (((keys >> (piece / PPR)) & 1u) == 0) w = u32x4_t{0, 0, 0, 0};
+          if constexpr (E4M3) {
+            const u32x2_t a0 = widen4(w.x), a1 = widen4(w.y), a2 = widen4(w.z), a3 = widen4(w.w);
+            ((u32x4_t*)to)[0] = u32x4_t{a0.x, a0.y, a1.x, a1.y};
+            ((u32x4_t*)to)[1] = u32x4_t{a2.x, a2.y, a3.x, a3.y};
+          } else {
+            *(u32x4_t*)to = w;
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_sched_barrier(0);
         ask_v(next_head, next);
         __builtin_amdgcn_sched_barrier(0);
-        if (!apart) {
+        // and transposed out of it: 16 lanes read 4 keys of 16 dimensions and get
+        // them by dimension
 #pragma unroll
-          for (int d = 0; d < DB; ++d) {
-            const bf16x8_t v = get_v(d);
+        for (int d = 0; d < DB; ++d) {
+          typedef short s16x8_t __attribute__((ext_vector_type(8)));
+          typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+          const uint16_t* from = vt + (grp * 4 + col / 4) * VS + d * 16 + col % 4 * 4;
+          const s16x4_t x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)from);
+          const s16x4_t x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(from + 16 * VS));
+          const s16x8_t x = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+          const bf16x8_t v = __builtin_bit_cast(bf16x8_t, x);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_hi[r], o[r][d], 0, 0, 0);
-              const f32x4_t s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_lo[r], o[r][d], 0, 0, 0);
-              o[r][d] = again && one_part[r] ? o[r][d] : s;
-            }
+          for (int r = 0; r < RT; ++r) {
+            o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_hi[r], o[r][d], 0, 0, 0);
+            o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p_lo[r], o[r][d], 0, 0, 0);
           }
         }
       }
       buf ^= 1;
     }
 
-    if (!again) {
-      bool odd = false;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        one_part[r] = false;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) one_part[r] = one_part[r] || !(fabsf(o[r][d][i]) < __builtin_inff());
-        odd = odd || one_part[r];
-      }
-      if (__builtin_amdgcn_ballot_w64(odd) != 0) {
-        again = true;
-        prime();
-        continue;
-      }
-    }
-    again = false;
+    // Rows to be summed by themselves: those whose scores are numbers and whose sums
+    // are not finite, for where V holds an infinity its products with the two parts
+    // of a P may cancel to NaN.
     const float v_scale = cv.v_scale != nullptr ? scalar_load(cv.v_scale + head) : 1.f;
+    uint32_t alone[RT];                                    // their columns
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const int row = (group0 + r) * 16 + col;
-      const float sum = row_sum(l[r]);
+      l[r] = row_sum(l[r]);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd[r] = odd[r] || !(fabsf(o[r][d][i]) < __builtin_inff());
+      const uint64_t lanes = __builtin_amdgcn_ballot_w64(odd[r] && l[r] == l[r] && row < rows);
+      alone[r] = (uint32_t)(lanes | (lanes >> 16) | (lanes >> 32) | (lanes >> 48)) & 0xffffu;
       if (row >= rows) continue;
+      const bool mine = ((alone[r] >> col) & 1u) == 0;
       const int64_t qr = (int64_t)item.seq * a.n_new + row / G;
       const int qh = head * G + row % G;
       const int64_t at = qr * a.q_heads + qh;
       if (span.n == 1) {
-        const float inv = sum == 0.f ? 0.f : v_scale / sum;
+        const float inv = l[r] == 0.f ? 0.f : v_scale / l[r];
         uint16_t* to = a.out + qr * a.ldo + (int64_t)qh * hd + grp * 4;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
-          if (d * 16 < hd)
+          if (mine && d * 16 < hd)
             *(u32x2_t*)(to + d * 16) = u32x2_t{pack_bf16(o[r][d].x * inv, o[r][d].y * inv),
                                                pack_bf16(o[r][d].z * inv, o[r][d].w * inv)};
-        if (grp == 0 && a.lse != nullptr) a.lse[at] = sum == 0.f ? kNegInf : m[r] * kLn2 + logf(sum);
+        if (grp == 0 && a.lse != nullptr) a.lse[at] = l[r] == 0.f ? kNegInf : m[r] * kLn2 + logf(l[r]);
       } else {
         const int64_t part_at = at * sp.max_chunks + item.c;
         float* to = sp.sums + part_at * hd + grp * 4;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
-          if (d * 16 < hd) *(f32x4_t*)(to + d * 16) = o[r][d];
-        if (grp == 0) *(f32x2_t*)(sp.stats + part_at * 2) = f32x2_t{m[r], sum};
+          if (mine && d * 16 < hd) *(f32x4_t*)(to + d * 16) = o[r][d];
+        if (grp == 0) *(f32x2_t*)(sp.stats + part_at * 2) = f32x2_t{m[r], l[r]};
       }
     }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      for (uint32_t cols = alone[r]; cols != 0; cols &= cols - 1) {
+        const int c = __builtin_ctz(cols);
+        plain_row<E4M3>(a, sp, item, head, (group0 + r) * 16 + c, __shfl(m[r], c), __shfl(l[r], c), z_scale, v_scale,
+                        lane);
+      }
     --left;
     next_item(item);
   }
