@@ -184,8 +184,8 @@ __device__ __forceinline__ void plain_row(const AttendArgs& a, const Split& sp, 
 // loads: the next tile's K is asked for as soon as this one's has gone into S,
 // its V as soon as this one's is in LDS.  No wave waits for another.
 template <int HB, bool E4M3, int RT>
-__global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_kernel(const AttendArgs a,
-                                                                                    const Split sp) {
+__global__ void __launch_bounds__(256, HB <= 4 ? 2 : 1) cache_attention_kernel(const AttendArgs a,
+                                                                                const Split sp) {
   constexpr int HP = HB * 32, DB = HB * 2;                 // padded head_dim; its blocks of 16
   constexpr int VS = HP + 16;                              // bf16 a row of V in LDS: rows start 8 banks apart
   constexpr int VP = E4M3 ? HB : 2 * HB, PPR = E4M3 ? 2 * HB : 4 * HB;   // V's 16-byte pieces a lane, a row
@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
   };
   prime();
 
-  int t_row[RT];                                           // this lane's row of each row tile: its token
-  bf16x8_t q[RT][HB];                                      // and its q, as the matrix operand
+  int t_row[RT], at_row[RT];                               // this lane's row of each row tile: its token, its
+  bf16x8_t q[RT][HB];                                      // place among (row, head) pairs (-1: no row), its q
   int q_seq = -1, q_part = -1;
   while (left > 0) {
     const Span span = item.span;
@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
         const int row = (group0 + r) * 16 + col;
         const int j = row / G;
         t_row[r] = span.len - a.n_new + j;
+        at_row[r] = row < rows ? (item.seq * a.n_new + j) * a.q_heads + head * G + row % G : -1;
         // a row past the last takes the first's values, set to 0
         const uint16_t* p = a.q + ((int64_t)item.seq * a.n_new + (row < rows ? j : 0)) * a.ldq +
                             (int64_t)(head * G + (row < rows ? row % G : 0)) * hd;
@@ -508,30 +509,27 @@ __global__ void __launch_bounds__(256, HB * RT <= 4 ? 2 : 1) cache_attention_ker
     uint32_t alone[RT];                                    // their columns
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const int row = (group0 + r) * 16 + col;
       l[r] = row_sum(l[r]);
+      float none = 0.f;                                    // NaN if any is not finite
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) odd[r] = odd[r] || !(fabsf(o[r][d][i]) < __builtin_inff());
-      const uint64_t lanes = __builtin_amdgcn_ballot_w64(odd[r] && l[r] == l[r] && row < rows);
+        for (int i = 0; i < 4; ++i) none = __builtin_fmaf(o[r][d][i], 0.f, none);
+      const uint64_t lanes = __builtin_amdgcn_ballot_w64((odd[r] || none != none) && l[r] == l[r] && at_row[r] >= 0);
       alone[r] = (uint32_t)(lanes | (lanes >> 16) | (lanes >> 32) | (lanes >> 48)) & 0xffffu;
-      if (row >= rows) continue;
+      if (at_row[r] < 0) continue;
       const bool mine = ((alone[r] >> col) & 1u) == 0;
-      const int64_t qr = (int64_t)item.seq * a.n_new + row / G;
-      const int qh = head * G + row % G;
-      const int64_t at = qr * a.q_heads + qh;
       if (span.n == 1) {
         const float inv = l[r] == 0.f ? 0.f : v_scale / l[r];
-        uint16_t* to = a.out + qr * a.ldo + (int64_t)qh * hd + grp * 4;
+        uint16_t* to = a.out + at_row[r] / a.q_heads * a.ldo + at_row[r] % a.q_heads * hd + grp * 4;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
           if (mine && d * 16 < hd)
             *(u32x2_t*)(to + d * 16) = u32x2_t{pack_bf16(o[r][d].x * inv, o[r][d].y * inv),
                                                pack_bf16(o[r][d].z * inv, o[r][d].w * inv)};
-        if (grp == 0 && a.lse != nullptr) a.lse[at] = l[r] == 0.f ? kNegInf : m[r] * kLn2 + logf(l[r]);
+        if (grp == 0 && a.lse != nullptr) a.lse[at_row[r]] = l[r] == 0.f ? kNegInf : m[r] * kLn2 + logf(l[r]);
       } else {
-        const int64_t part_at = at * sp.max_chunks + item.c;
+        const int64_t part_at = (int64_t)at_row[r] * sp.max_chunks + item.c;
         float* to = sp.sums + part_at * hd + grp * 4;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -610,7 +608,7 @@ int64_t attention_workspace(int64_t seqs, int64_t capacity, int q_heads, int hd,
 // a chunk for each wave: one that starts later starts its loads from nothing.
 template <int HB, bool E4M3, int RT>
 static void attend(const AttendArgs& a, const Split& sp, int64_t most, int cus, hipStream_t stream) {
-  constexpr int kHeld = HB * RT <= 2 ? 3 : HB * RT <= 4 ? 2 : 1;
+  constexpr int kHeld = HB * RT <= 2 ? 3 : HB <= 4 ? 2 : 1;
   const int grid = (int)std::min<int64_t>((most + 3) / 4, (int64_t)cus * kHeld);
   cache_attention_kernel<HB, E4M3, RT><<<grid, 256, 0, stream>>>(a, sp);
 }
