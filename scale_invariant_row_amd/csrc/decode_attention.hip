@@ -44,7 +44,7 @@ __device__ __forceinline__ Span span_here(const AttendArgs& a, int seq) {
   const int cap = a.cache.pages_per_seq << a.cache.page_shift;
   int len = scalar_load(a.lens + seq);
   len = len < 0 ? 0 : len > cap ? cap : len;
-  return span_of(len, a.n_new, a.window);
+  return span_of(len, a.n_new, a.window, a.cache.heads);
 }
 
 // Maximum and sum over the four lanes that hold a row's keys.
@@ -81,7 +81,7 @@ struct Item {
 __device__ __forceinline__ int chunks_of(const AttendArgs& a, int s0, int lane) {
   if (s0 + lane >= a.cache.seqs) return 0;
   const int len = a.lens[s0 + lane], cap = a.cache.pages_per_seq << a.cache.page_shift;
-  return span_of(len < 0 ? 0 : len > cap ? cap : len, a.n_new, a.window).n;
+  return span_of(len < 0 ? 0 : len > cap ? cap : len, a.n_new, a.window, a.cache.heads).n;
 }
 
 __device__ __forceinline__ int64_t list_length(const AttendArgs& a, int parts, int lane) {
@@ -184,14 +184,14 @@ __device__ __forceinline__ void plain_row(const AttendArgs& a, const Split& sp, 
 // loads: the next tile's K is asked for as soon as this one's has gone into S,
 // its V as soon as this one's is in LDS.  No wave waits for another.
 template <int HB, bool E4M3, int RT>
-__global__ void __launch_bounds__(256, HB <= 4 ? 2 : 1) cache_attention_kernel(const AttendArgs a,
-                                                                                const Split sp) {
+__global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_attention_kernel(const AttendArgs a,
+                                                                                    const Split sp) {
   constexpr int HP = HB * 32, DB = HB * 2;                 // padded head_dim; its blocks of 16
   constexpr int VS = HP + 16;                              // bf16 a row of V in LDS: rows start 8 banks apart
   constexpr int VP = E4M3 ? HB : 2 * HB, PPR = E4M3 ? 2 * HB : 4 * HB;   // V's 16-byte pieces a lane, a row
   constexpr int EB = E4M3 ? 1 : 2;                         // bytes an element
   __shared__ __attribute__((aligned(16))) uint16_t v_tiles[4][kTile * VS];
-  __shared__ int64_t places[4][2][kLeastChunk];            // byte offset of a key's token
+  __shared__ int64_t places[4][2][kBlock];            // byte offset of a key's token
   const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const CacheView& cv = a.cache;
@@ -342,14 +342,14 @@ __global__ void __launch_bounds__(256, HB <= 4 ? 2 : 1) cache_attention_kernel(c
       for (int d = 0; d < DB; ++d) o[r][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     const int hi = chunk_hi(item);
-    for (int kb = chunk_lo(item); kb < hi; kb += kLeastChunk) {
+    for (int kb = chunk_lo(item); kb < hi; kb += kBlock) {
       valid[0] = soon_valid[0];
       valid[1] = soon_valid[1];
       const int64_t block_head = soon_head;
-      soon_k0 += kLeastChunk;
+      soon_k0 += kBlock;
       soon_from();
       ask_pages();
-      const int tiles = (min(hi - kb, kLeastChunk) + kTile - 1) / kTile;
+      const int tiles = (min(hi - kb, kBlock) + kTile - 1) / kTile;
       for (int tile = 0; tile < tiles; ++tile) {
         const int k0 = kb + tile * kTile;
         const uint32_t keys = (uint32_t)((tile < 2 ? valid[0] : valid[1]) >> (tile % 2 * 32));
@@ -599,8 +599,9 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const AttendA
   if (lane == 0 && a.lse != nullptr) a.lse[at] = sum == 0.f ? kNegInf : top * kLn2 + logf(sum);
 }
 
-int64_t attention_workspace(int64_t seqs, int64_t capacity, int q_heads, int hd, int n_new, int window) {
-  const int n = most_chunks(capacity, n_new, window);
+int64_t attention_workspace(int64_t seqs, int64_t capacity, int q_heads, int heads, int hd, int n_new,
+                            int window) {
+  const int n = most_chunks(capacity, n_new, window, heads);
   return n == 1 ? 0 : seqs * n_new * q_heads * n * (hd + 2) * 4;
 }
 
@@ -608,7 +609,7 @@ int64_t attention_workspace(int64_t seqs, int64_t capacity, int q_heads, int hd,
 // a chunk for each wave: one that starts later starts its loads from nothing.
 template <int HB, bool E4M3, int RT>
 static void attend(const AttendArgs& a, const Split& sp, int64_t most, int cus, hipStream_t stream) {
-  constexpr int kHeld = HB * RT <= 2 ? 3 : HB <= 4 ? 2 : 1;
+  constexpr int kHeld = HB * RT <= 2 ? 3 : HB <= (RT == 1 ? 4 : 2) ? 2 : 1;
   const int grid = (int)std::min<int64_t>((most + 3) / 4, (int64_t)cus * kHeld);
   cache_attention_kernel<HB, E4M3, RT><<<grid, 256, 0, stream>>>(a, sp);
 }
@@ -639,7 +640,7 @@ hipError_t launch_cache_attention(const AttendArgs& args, int cus, void* workspa
   const int64_t capacity = (int64_t)cv.pages_per_seq << cv.page_shift;
   const int tiles = (a.q_heads / cv.heads * a.n_new + 15) / 16;
   Split sp;
-  sp.max_chunks = most_chunks(capacity, a.n_new, a.window);
+  sp.max_chunks = most_chunks(capacity, a.n_new, a.window, cv.heads);
   const int64_t heads = (int64_t)cv.seqs * a.n_new * a.q_heads;
   sp.sums = static_cast<float*>(workspace);
   sp.stats = sp.sums + heads * sp.max_chunks * cv.hd;

@@ -289,7 +289,7 @@ int64_t ds_cache_attention_rows_workspace(const ds_kv_cache* cache, int32_t n_q_
   if (window < 0) return DS_ERR_ARG;
   if ((int64_t)c.n_seqs * new_tokens > kMostHeadRows / n_q_heads) return DS_ERR_SHAPE;
   return dsr::attention_workspace(c.n_seqs, (int64_t)c.pages_per_seq * c.page_size, n_q_heads,
-                                  c.head_dim, new_tokens, window);
+                                  c.n_heads, c.head_dim, new_tokens, window);
 }
 
 int ds_cache_attention_rows(const ds_kv_cache* cache, const uint16_t* q, int64_t ldq,

@@ -202,7 +202,7 @@ def test_workspace_sizes_refuse_what_the_calls_refuse(L):
     assert size(4, 1, 0, pages_per_seq=17) == 3 * 4 * 3 * 66 * 4                # three
     assert size(4, 1, 97, pages_per_seq=1000) == 0                              # a window within one
     assert size(4, 1, 98, pages_per_seq=1000) == 3 * 4 * 2 * 66 * 4
-    assert size(4, 1, 0, pages_per_seq=1 << 25) == size(4, 1, 0, pages_per_seq=1 << 11)   # 128 chunks at most
+    assert size(4, 1, 0, pages_per_seq=1 << 25) == size(4, 1, 0, pages_per_seq=1 << 12)   # 128 chunks at most
     assert size(4, 1, 0, n_seqs=1 << 21) == 0 and size(4, 1, 0, n_seqs=(1 << 21) + 1) == S
     del cache
     f = L.ds_draft_verify_rows_workspace

@@ -66,17 +66,26 @@ int main() {
   for (int cap : {0, 1, 16, 255, 256, 257, 4096, 32768, 32769, 131072, 1 << 30})
     for (int len : {0, 1, 2, 5, 31, 32, 33, 255, 256, 257, 1000, 32768, 32769, 100000, 1 << 30})
       for (int n_new : {1, 2, 16})
-        for (int window : {0, 1, 31, 33, 1000, 40000, 1 << 29}) {
-          if (len > cap) continue;
-          const Span s = span_of(len, n_new, window);
-          const int64_t first = window ? (int64_t)len - n_new - window + 1 : 0;
-          NEED(s.first == (first > 0 ? first : 0) && s.start % kTile == 0 && s.start <= s.first);
-          NEED(s.first - s.start < kTile && s.chunk % kLeastChunk == 0 && s.chunk > 0);
-          NEED(s.n >= 1 && s.n <= kMaxChunks && s.n <= most_chunks(cap, n_new, window));
-          NEED((int64_t)s.start + (int64_t)s.n * s.chunk >= len);
-          NEED(s.n == 1 || (int64_t)s.start + (int64_t)(s.n - 1) * s.chunk < len);   // none empty
-          NEED((int64_t)s.start + (int64_t)s.n * s.chunk <= INT32_MAX);
-        }
+        for (int window : {0, 1, 31, 33, 1000, 40000, 1 << 29})
+          for (int heads : {1, 4, 12, 96, 1 << 20}) {
+            if (len > cap) continue;
+            const Span s = span_of(len, n_new, window, heads);
+            const int64_t first = window ? (int64_t)len - n_new - window + 1 : 0;
+            NEED(s.first == (first > 0 ? first : 0) && s.start % kTile == 0 && s.start <= s.first);
+            NEED(s.first - s.start < kTile && s.chunk % kBlock == 0 && s.chunk > 0);
+            NEED(s.n >= 1 && s.n <= kMaxChunks && s.n <= most_chunks(cap, n_new, window, heads));
+            NEED((int64_t)s.start + (int64_t)s.n * s.chunk >= len);
+            NEED(s.n == 1 || (int64_t)s.start + (int64_t)(s.n - 1) * s.chunk < len);   // none empty
+            NEED((int64_t)s.start + (int64_t)s.n * s.chunk <= INT32_MAX);
+          }
+  // every length up to a capacity fits what is sized for it
+  for (int heads : {1, 3, 8, 40})
+    for (int window : {0, 500, 20000})
+      for (int len = 0, most = 0; len < 70000; len += 1 + len / 97) {
+        const int n = span_of(len, 3, window, heads).n;
+        most = most > n ? most : n;
+        NEED(most <= most_chunks(len, 3, window, heads));
+      }
   std::printf("places %ld\n", places);
   return 0;
 }
