@@ -131,15 +131,35 @@ struct Exchange {
   float f[kHeadRows][PAIRS == kOddHalves ? 1024 : 1];
 };
 
-// One wave a row, q's heads then k's.
+// A row's heads in groups of `group`, q's then k's (and v's): 1 << share waves
+// take them in turn.  The wave's row and its first head of each kind:
+struct Part {
+  int64_t row;
+  int mine, waves, before;      // before: groups of the kinds gone by
+  __device__ __forceinline__ Part(int wave, int share) {
+    const int64_t i = (int64_t)blockIdx.x * kHeadRows + wave;
+    row = i >> share;
+    waves = 1 << share;
+    mine = (int)i & (waves - 1);
+    before = 0;
+  }
+  __device__ __forceinline__ int first(int nh, int group) {
+    const int g = (mine - before) & (waves - 1);
+    before += (nh + group - 1) / group;
+    return g * group;
+  }
+};
+
+// 1 << share waves a row.
 template <int LPH, int PAIRS>
-__global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a, int share) {
   constexpr int HPW = 64 / LPH, CH = 4;
   __shared__ __attribute__((aligned(16))) float trig[kHeadRows][2][128];
   __shared__ __attribute__((aligned(16))) Exchange<PAIRS> xch;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = (int64_t)blockIdx.x * kHeadRows + wave;
+  Part part(wave, share);
+  const int64_t row = part.row;
   if (row >= a.rows) return;
   const Place<LPH, PAIRS> at(lane, a.hd, a.turn.rotary);
   const int hs = lane / LPH;
@@ -157,7 +177,7 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a) {
     }
   };
   const RowBuf qb(a.x[0] + row * a.ldx[0], (uint32_t)a.nh[0] * head_bytes);
-  load(qb, 0);
+  load(qb, part.mine * CH * HPW);                          // past q's heads: not used
   fill_turn(trig[wave], position(a.pos, row), a.turn, lane);
   float c[8], s[8];
   lane_angles(trig[wave], at, a.turn.rotary, c, s);
@@ -168,8 +188,9 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a) {
     if (nh == 0) continue;
     const RowBuf ib(a.x[which] + row * a.ldx[which], (uint32_t)nh * head_bytes);
     const RowBuf ob(a.y[which] + row * a.ldy[which], (uint32_t)nh * head_bytes);
-    for (int h0 = 0; h0 < nh; h0 += CH * HPW) {
-      if (which > 0 || h0 > 0) load(ib, h0);
+    const int start = part.first(nh, CH * HPW);
+    for (int h0 = start; h0 < nh; h0 += CH * HPW << share) {
+      if (which > 0 || h0 > start) load(ib, h0);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         if (h0 + i * HPW >= nh) break;                     // uniform
@@ -214,15 +235,18 @@ __device__ __forceinline__ int64_t token_offset(const CacheView& c, int64_t seq,
   return token_bytes_at(c, position(c.table, table_entry(c, seq, p)), p);
 }
 
-// One wave a row: its q heads, its k heads, its v heads.
+// 1 << share waves a row.  Five waves a SIMD: 24 prompts of up to 1,021 tokens,
+// 16 + 2 * 4 heads of 256 into e4m3, 65.5 us with the four that the compiler
+// comes to by itself, 54.2 with five, 57.4 with six (registers spilled).
 template <int LPH, int PAIRS, bool RMS>
-__global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256, PAIRS == kOddHalves ? 4 : 5) cache_append_kernel(const AppendArgs a, int share) {
   constexpr int HPW = 64 / LPH, CH = 2;
   __shared__ __attribute__((aligned(16))) float trig[kHeadRows][2][128];
   __shared__ __attribute__((aligned(16))) Exchange<PAIRS> xch;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = (int64_t)blockIdx.x * kHeadRows + wave;
+  Part part(wave, share);
+  const int64_t row = part.row;
   if (row >= a.rows) return;
   const CacheView& cv = a.cache;
   const int hd = cv.hd, rotary = a.turn.rotary;
@@ -245,6 +269,8 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
   for (int which = 0; which < 3; ++which) {
     const int nh = which == 0 ? a.q_heads : cv.heads;
     if (nh == 0 || (which > 0 && token < 0)) continue;     // uniform
+    const int start = part.first(nh, CH * HPW);
+    if (start >= nh) continue;
     float w[16];
     if (RMS && which < 2) {
       load_weights(a.w[which], at.a, at.active, w);
@@ -255,12 +281,14 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
                     which == 0 ? (uint32_t)nh * head_bytes : 0u);
     char* to = which == 1 ? cv.k : cv.v;
     const float* scales = which == 1 ? cv.k_scale : cv.v_scale;
-    for (int h0 = 0; h0 < nh; h0 += CH * HPW) {
+    for (int h0 = start; h0 < nh; h0 += CH * HPW << share) {
       u32x4_t x[CH][2];
+      float scale[CH];
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         x[i][0] = ib.ld16(off(h0 + i * HPW, lane_a));
         x[i][1] = ib.ld16(off(h0 + i * HPW, lane_b));
+        scale[i] = which > 0 && scales != nullptr ? scales[min(h0 + i * HPW + hs, nh - 1)] : 1.f;
       }
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -284,9 +312,9 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendArgs a) {
         } else if (at.active && h + hs < nh) {
           char* t = to + token + (int64_t)(h + hs) * cv.head_bytes;
           if (cv.e4m3) {
-            const float scale = scales != nullptr ? scales[h + hs] : 1.f, inv = 1.f / scale;
-            *(u32x2_t*)(t + at.a) = pack8_e4m3(v, scale, inv);
-            *(u32x2_t*)(t + at.b) = pack8_e4m3(v + 8, scale, inv);
+            const float inv = 1.f / scale[i];
+            *(u32x2_t*)(t + at.a) = pack8_e4m3(v, scale[i], inv);
+            *(u32x2_t*)(t + at.b) = pack8_e4m3(v + 8, scale[i], inv);
           } else {
             *(u32x4_t*)(t + at.a * 2) = pack8(v);
             *(u32x4_t*)(t + at.b * 2) = pack8(v + 8);
@@ -307,49 +335,73 @@ static int pairing(const Turn& t) {
   return t.interleaved ? kNeighbours : t.rotary % 16 == 0 ? kHalves : kOddHalves;
 }
 
+constexpr int kFew = 4;
+
+static int groups(int heads, int group) { return (heads + group - 1) / group; }
+
+// log2 of the waves that share a row of `n` groups: as many as have one each,
+// up to a workgroup's four, where that leaves at most kFew waves a SIMD.  64
+// rows of 16 + 2 * 4 heads of 256 take 9.9 us by one wave each, 6.4 by four;
+// 24,500 rows of 32 + 2 * 8 heads of 128 take 53 by one, 59 by four (each finds
+// its row's angles again).
+static int waves_of(int64_t rows, int n, int cus) {
+  int share = 0;
+  while (share < 2 && 1 << share < n && rows << (share + 1) <= (int64_t)cus * 4 * kFew) ++share;
+  return share;
+}
+
+static int grid_of(int64_t rows, int share) {
+  return (int)(((rows << share) + kHeadRows - 1) / kHeadRows);
+}
+
 template <int LPH>
-static hipError_t rope_lanes(const RopeArgs& a, int grid, hipStream_t stream) {
+static hipError_t rope_lanes(const RopeArgs& a, int cus, hipStream_t stream) {
+  const int share = waves_of(a.rows, groups(a.nh[0], 256 / LPH) + groups(a.nh[1], 256 / LPH), cus);
+  const int grid = grid_of(a.rows, share);
   switch (pairing(a.turn)) {
-    case kHalves: rope_rows_kernel<LPH, kHalves><<<grid, 256, 0, stream>>>(a); break;
-    case kNeighbours: rope_rows_kernel<LPH, kNeighbours><<<grid, 256, 0, stream>>>(a); break;
-    default: rope_rows_kernel<LPH, kOddHalves><<<grid, 256, 0, stream>>>(a); break;
+    case kHalves: rope_rows_kernel<LPH, kHalves><<<grid, 256, 0, stream>>>(a, share); break;
+    case kNeighbours: rope_rows_kernel<LPH, kNeighbours><<<grid, 256, 0, stream>>>(a, share); break;
+    default: rope_rows_kernel<LPH, kOddHalves><<<grid, 256, 0, stream>>>(a, share); break;
   }
   return hipGetLastError();
 }
 
-hipError_t launch_rope_rows(const RopeArgs& a, int grid, hipStream_t stream) {
+hipError_t launch_rope_rows(const RopeArgs& a, int cus, hipStream_t stream) {
   switch (lanes_per_head(a.hd)) {
-    case 1: return rope_lanes<1>(a, grid, stream);
-    case 2: return rope_lanes<2>(a, grid, stream);
-    case 4: return rope_lanes<4>(a, grid, stream);
-    case 8: return rope_lanes<8>(a, grid, stream);
-    case 16: return rope_lanes<16>(a, grid, stream);
+    case 1: return rope_lanes<1>(a, cus, stream);
+    case 2: return rope_lanes<2>(a, cus, stream);
+    case 4: return rope_lanes<4>(a, cus, stream);
+    case 8: return rope_lanes<8>(a, cus, stream);
+    case 16: return rope_lanes<16>(a, cus, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
 template <int LPH, bool RMS>
-static hipError_t append_lanes(const AppendArgs& a, int grid, hipStream_t stream) {
+static hipError_t append_lanes(const AppendArgs& a, int cus, hipStream_t stream) {
+  const int share = waves_of(
+      a.rows, groups(a.q_heads, 128 / LPH) + 2 * groups(a.cache.heads, 128 / LPH), cus);
+  const int grid = grid_of(a.rows, share);
   switch (pairing(a.turn)) {
-    case kHalves: cache_append_kernel<LPH, kHalves, RMS><<<grid, 256, 0, stream>>>(a); break;
-    case kNeighbours: cache_append_kernel<LPH, kNeighbours, RMS><<<grid, 256, 0, stream>>>(a); break;
-    default: cache_append_kernel<LPH, kOddHalves, RMS><<<grid, 256, 0, stream>>>(a); break;
+    case kHalves: cache_append_kernel<LPH, kHalves, RMS><<<grid, 256, 0, stream>>>(a, share); break;
+    case kNeighbours: cache_append_kernel<LPH, kNeighbours, RMS><<<grid, 256, 0, stream>>>(a, share); break;
+    default: cache_append_kernel<LPH, kOddHalves, RMS><<<grid, 256, 0, stream>>>(a, share); break;
   }
   return hipGetLastError();
 }
 
 template <int LPH>
-static hipError_t append_norm(const AppendArgs& a, int grid, hipStream_t stream) {
-  return a.rms ? append_lanes<LPH, true>(a, grid, stream) : append_lanes<LPH, false>(a, grid, stream);
+static hipError_t append_norm(const AppendArgs& a, int cus, hipStream_t stream) {
+  return a.rms ? append_lanes<LPH, true>(a, cus, stream) : append_lanes<LPH, false>(a, cus, stream);
 }
 
-hipError_t launch_cache_append(const AppendArgs& a, int grid, hipStream_t stream) {
+hipError_t launch_cache_append(const AppendArgs& a, int cus, hipStream_t stream) {
   switch (lanes_per_head(a.cache.hd)) {
-    case 1: return append_norm<1>(a, grid, stream);
-    case 2: return append_norm<2>(a, grid, stream);
-    case 4: return append_norm<4>(a, grid, stream);
-    case 8: return append_norm<8>(a, grid, stream);
-    case 16: return append_norm<16>(a, grid, stream);
+    case 1: return append_norm<1>(a, cus, stream);
+    case 2: return append_norm<2>(a, cus, stream);
+    case 4: return append_norm<4>(a, cus, stream);
+    case 8: return append_norm<8>(a, cus, stream);
+    case 16: return append_norm<16>(a, cus, stream);
     default: return hipErrorInvalidValue;
   }
 }

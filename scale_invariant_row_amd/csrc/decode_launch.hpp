@@ -127,8 +127,8 @@ struct AppendArgs {
 };
 
 constexpr int kHeadRows = 4;    // rows a workgroup of both kernels
-hipError_t launch_rope_rows(const RopeArgs& a, int grid, hipStream_t stream);
-hipError_t launch_cache_append(const AppendArgs& a, int grid, hipStream_t stream);
+hipError_t launch_rope_rows(const RopeArgs& a, int cus, hipStream_t stream);
+hipError_t launch_cache_append(const AppendArgs& a, int cus, hipStream_t stream);
 
 struct AttendArgs {
   CacheView cache;

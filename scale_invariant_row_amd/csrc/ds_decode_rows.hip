@@ -72,7 +72,7 @@ int rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const i
     a.nh[0] = nq;
     a.nh[1] = nk;
     a.hd = head_dim;
-    return dsr::launch_rope_rows(a, (int)((n + dsr::kHeadRows - 1) / dsr::kHeadRows),
+    return dsr::launch_rope_rows(a, cus,
                                  (hipStream_t)stream);
   }));
 }
@@ -272,7 +272,7 @@ int ds_cache_append_rows(const ds_kv_cache* cache, const uint16_t* q, int64_t ld
     a.q_heads = n_q_heads;
     a.rms = rms;
     a.eps = eps;
-    return dsr::launch_cache_append(a, (int)((n + dsr::kHeadRows - 1) / dsr::kHeadRows),
+    return dsr::launch_cache_append(a, cus,
                                     (hipStream_t)stream);
   }));
 }
