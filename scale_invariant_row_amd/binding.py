@@ -258,12 +258,14 @@ def _check(status: int, what: str) -> None:
 # --------------------------------------------------------------- tensors
 
 _torch_module = None
+_half_types = None            # what holds bf16 data
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _half_types
     if _torch_module is None:
         import torch
+        _half_types = frozenset((torch.bfloat16, torch.int16, torch.uint16))
         _torch_module = torch
     return _torch_module
 
@@ -884,15 +886,15 @@ def ds_embed_rows_backward(dy, ids, vocab: int, scale: float = 1.0, dtable=None,
 
 def _heads(t, name: str, head_dim: int, rows: Optional[int] = None) -> int:
     """Number of heads of a bf16 [rows, heads * head_dim] view (rows may be strided)."""
-    torch = _torch()
-    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or t.dim() != 2 \
-            or (t.numel() > 0 and t.stride(1) != 1):
+    _torch()
+    if t.dtype not in _half_types or t.dim() != 2 or (t.stride(1) != 1 and t.numel() > 0):
         raise ValueError(f"{name}: expected a bf16 [rows, cols] tensor with unit column stride")
-    if rows is not None and t.shape[0] != rows:
-        raise ValueError(f"{name}: expected {rows} rows like q, got {t.shape[0]}")
-    if t.shape[1] % head_dim:
+    n, width = t.shape
+    if rows is not None and n != rows:
+        raise ValueError(f"{name}: expected {rows} rows like q, got {n}")
+    if width % head_dim:
         raise ValueError(f"{name}: its width must be a whole number of heads")
-    return t.shape[1] // head_dim
+    return width // head_dim
 
 
 def _row_stride(t) -> int:

@@ -239,3 +239,25 @@ def test_no_rows(B):
     i = torch.empty(0, dtype=torch.int32, device="cuda:0")
     assert B.ds_cache_append_rows(paged.cache, e, e, i, q=e).shape == (0, 64)
     assert B.ds_cache_append_rows(paged.cache, e, e, i) is None
+
+
+@pytest.mark.parametrize("heads,nq,hd,kind", [(10, 70, 64, "bf16"), (70, 3, 32, "e4m3"), (5, 5, 256, "bf16")])
+def test_many_rows_are_as_a_few(B, heads, nq, hd, kind):
+    """More heads than a pass of one to four waves, however many rows there are."""
+    import torch
+    c = Case([1700, 1, 1501, 3], heads, nq, hd, hd, 16, 11, kind)
+    announce("append of many rows", heads, nq, hd, kind)
+    whole, parts = c.paged(B), c.paged(B)
+    q = c.run(B, whole)
+    b, pieces, a = torch.bfloat16, [], 0
+    for n in (7, 600, 1700, len(c.pos) - 2307):            # four, two or one wave a row, by the device's size
+        i, a = slice(a, a + n), a + n
+        pieces.append(B.ds_cache_append_rows(
+            parts.cache, dev(c.k[i], b), dev(c.v[i], b), dev(c.pos[i]), seqs=dev(c.seqs[i]), inv_freq=dev(c.inv),
+            q=dev(c.q[i], b), rms_eps=1e-6, q_weight=dev(c.qw), k_weight=dev(c.kw)))
+    torch.cuda.synchronize()
+    assert torch.equal(bits(q), bits(torch.cat(pieces)))
+    for x, y in zip(whole.bits(), parts.bits()):
+        assert np.array_equal(x, y)
+    want, mag = c.heads_of(c.q, c.qw)
+    close(host(q), want, 52 * U * mag, "q", bf16=True)

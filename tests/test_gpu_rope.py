@@ -147,3 +147,23 @@ def test_no_rows(B):
     e = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda:0")
     q, k = B.ds_rope_rows(e, e, torch.empty(0, dtype=torch.int32, device="cuda:0"), torch.ones(32, device="cuda:0"), 64)
     assert q.shape == (0, 128) and k.shape == (0, 128)
+
+
+@pytest.mark.parametrize("nq,nk,hd", [(70, 10, 64), (3, 70, 128), (12, 12, 16), (90, 0, 32)])
+def test_many_rows_are_as_a_few(B, nq, nk, hd):
+    """More heads than a pass of one to four waves, however many rows there are."""
+    import torch
+    c = Case(5003, nq, nk, hd, hd, 8)
+    q, k, pos, inv, _ = c.args()
+    announce("rope of many rows", nq, nk, hd)
+    whole = B.ds_rope_rows(q, k, pos, inv, hd)
+    for n in (3, 1100, 3001):                              # four, two or one wave a row, by the device's size
+        a = 5003 - n
+        part = B.ds_rope_rows(q[a:], None if k is None else k[a:], pos[a:], inv, hd)
+        torch.cuda.synchronize()
+        for x, y in zip(whole, part):
+            assert y is None or torch.equal(bits(x[a:].contiguous()), bits(y))
+    few = Case.__new__(Case)
+    few.__dict__.update(c.__dict__)
+    few.q, few.k, few.pos = c.q[-37:], c.k[-37:], c.pos[-37:]
+    few.check([None if y is None else y[-37:].contiguous() for y in whole], False)
