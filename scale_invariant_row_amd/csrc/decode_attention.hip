@@ -27,6 +27,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kRise = 8.f;         // of z log2 e
+constexpr float kReduce = 0x1p-32f;
 
 struct Split {
   float* sums;                       // [row][head][max_chunks][hd]
@@ -123,7 +124,8 @@ __device__ __forceinline__ Item item_at(const AttendArgs& a, int parts, int64_t 
 
 // O of one row's head over one chunk, key by key in fp32 (the wave's lanes share
 // its dimensions), from its m and l: what the matrix instructions cannot keep
-// apart is handed here.
+// apart is handed here.  Its sums are kReduce times O (weights reach 2^kRise, a
+// chunk 2^23 keys): what is written of them for a join has l < 0.
 template <bool E4M3>
 __device__ __forceinline__ void plain_row(const AttendArgs& a, const Split& sp, const Item& item, int head, int row,
                                           float m, float l, float z_scale, float v_scale, int lane) {
@@ -160,7 +162,7 @@ __device__ __forceinline__ void plain_row(const AttendArgs& a, const Split& sp, 
       if (i * 64 + lane < hd) z = __builtin_fmaf(q[i], value(k, i * 64 + lane), z);
     z = wave_sum(z) * z_scale;
     if (z == kNegInf) continue;                            // masked
-    const float p = exp2_fast(z - base);
+    const float p = exp2_fast(z - base) * kReduce;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (i * 64 + lane < hd) o[i] += p * value(v, i * 64 + lane);
@@ -171,10 +173,11 @@ __device__ __forceinline__ void plain_row(const AttendArgs& a, const Split& sp, 
     const int d = i * 64 + lane;
     if (d >= hd) continue;
     if (item.span.n == 1)
-      a.out[qr * a.ldo + (int64_t)qh * hd + d] = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[i] / l * v_scale, 0.f);
+      a.out[qr * a.ldo + (int64_t)qh * hd + d] = (uint16_t)pack_bf16(l == 0.f ? 0.f : o[i] / (l * kReduce) * v_scale, 0.f);
     else
       sp.sums[part_at * hd + d] = o[i];
   }
+  if (item.span.n > 1 && lane == 0) *(f32x2_t*)(sp.stats + part_at * 2) = f32x2_t{m, -l};
 }
 
 // HB: head_dim in blocks of 32, rounded up.  RT: tiles of 16 rows a wave.
@@ -353,11 +356,10 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
       for (int tile = 0; tile < tiles; ++tile) {
         const int k0 = kb + tile * kTile;
         const uint32_t keys = (uint32_t)((tile < 2 ? valid[0] : valid[1]) >> (tile % 2 * 32));
-        // every row sees every key; some rows see a key that others do not
+        // every row sees every key; there may be keys that some row does not see
         const bool whole = keys == 0xffffffffu && k0 + kTile - 1 <= t_first &&
                            (a.window == 0 || k0 > t_last - a.window);
-        const bool mixed = t_first < t_last &&
-                           (k0 + kTile - 1 > t_first || (a.window != 0 && k0 <= t_last - a.window));
+        const bool mixed = a.n_new > 1 && (k0 + kTile - 1 > t_first || (a.window != 0 && k0 <= t_last - a.window));
         f32x4_t z[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r) z[r][0] = z[r][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -426,8 +428,9 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
           }
         }
         // A key that a row does not see must not reach it even as 0 times an
-        // infinity.  A key that no row sees is made zeros; one that some see, and
-        // that holds infinities or NaN, too, and those rows are summed by themselves.
+        // infinity.  What is not among the sequence's keys is made zeros; so is one
+        // that holds infinities or NaN and that some row does not see, and the rows
+        // that see it are summed by themselves.
         if (mixed) {
           const int from = a.window != 0 ? t_last - a.window : -1;
           uint32_t bad_keys = 0;
@@ -503,8 +506,8 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
     }
 
     // Rows to be summed by themselves: those whose scores are numbers and whose sums
-    // are not finite, for where V holds an infinity its products with the two parts
-    // of a P may cancel to NaN.
+    // are not finite, for an infinity's products with the two parts of a P may cancel
+    // to NaN, and a sum of large V may overflow where its quotient by l does not.
     const float v_scale = cv.v_scale != nullptr ? scalar_load(cv.v_scale + head) : 1.f;
     uint32_t alone[RT];                                    // their columns
 #pragma unroll
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
 #pragma unroll
         for (int d = 0; d < DB; ++d)
           if (mine && d * 16 < hd) *(f32x4_t*)(to + d * 16) = o[r][d];
-        if (grp == 0) *(f32x2_t*)(sp.stats + part_at * 2) = f32x2_t{m[r], l[r]};
+        if (grp == 0 && mine) *(f32x2_t*)(sp.stats + part_at * 2) = f32x2_t{m[r], l[r]};
       }
     }
 #pragma unroll
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
   }
 }
 
-// Joins the chunks of a row's head: out = sum f_c O_c / sum f_c l_c with
+// Joins the chunks of a row's head: out = sum w_c O_c with w_c = f_c / sum f_c l_c,
 // f_c = exp(m_c - max m).  One workgroup a head; wave w adds chunks w, w + 4, ...
 __global__ void __launch_bounds__(256) cache_attention_join_kernel(const AttendArgs a, const Split sp) {
   __shared__ float factor[kMaxChunks];
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const AttendA
   const Span span = span_here(a, (int)(row / a.n_new));
   if (span.n == 1) return;                                 // written already
   const float* stats = sp.stats + at * sp.max_chunks * 2;
-  float m[kMaxChunks / 64], l[kMaxChunks / 64], top = kNegInf;
+  float m[kMaxChunks / 64], l[kMaxChunks / 64], f[kMaxChunks / 64], top = kNegInf;
 #pragma unroll
   for (int i = 0; i < kMaxChunks / 64; ++i) {
     const int c = i * 64 + lane;
@@ -575,11 +578,14 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const AttendA
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kMaxChunks / 64; ++i) {
-    const float f = exp2_fast(m[i] - base);
-    if (wave == 0) factor[i * 64 + lane] = f;
-    sum += f * l[i];
+    f[i] = exp2_fast(m[i] - base);
+    sum += f[i] * fabsf(l[i]);
   }
   sum = wave_sum(sum);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < kMaxChunks / 64; ++i)
+    if (wave == 0) factor[i * 64 + lane] = f[i] * inv * (l[i] < 0.f ? 1.f / kReduce : 1.f);
   __syncthreads();
   const int hd = a.cache.hd, d = lane * 4;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
@@ -593,9 +599,8 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const AttendA
   if (wave != 0 || d >= hd) return;
   for (int w = 1; w < 4; ++w) s += *(const f32x4_t*)(part[w] + d);
   const float v_scale = a.cache.v_scale != nullptr ? a.cache.v_scale[qh / (a.q_heads / a.cache.heads)] : 1.f;
-  const float inv = sum == 0.f ? 0.f : v_scale / sum;
   *(u32x2_t*)(a.out + row * a.ldo + (int64_t)qh * hd + d) =
-      u32x2_t{pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv)};
+      u32x2_t{pack_bf16(s.x * v_scale, s.y * v_scale), pack_bf16(s.z * v_scale, s.w * v_scale)};
   if (lane == 0 && a.lse != nullptr) a.lse[at] = sum == 0.f ? kNegInf : top * kLn2 + logf(sum);
 }
 

@@ -167,6 +167,35 @@ def test_what_a_row_does_not_see_does_not_reach_it(B, bad, kind, new, window):
         assert np.isnan(x[new - 1]).all()
 
 
+@pytest.mark.parametrize("group,new,window", [(40, 2, 0), (17, 4, 50), (2, 9, 0)])
+def test_a_new_token_does_not_reach_earlier_ones(B, group, new, window):
+    """Heads of one token that fill tiles of their own, and tiles of several."""
+    c = Case([200, 31], 1, group, 64, 16, 17, new, window)
+    clean = [host(x) for x in c.run(B)]
+    c.check(c.run(B))
+    last = D.token_place(c.table, c.n_pages, 16, 0, 199)
+    c.k[last], c.v[last] = np.nan, np.inf
+    announce("attention of earlier tokens", group, new, window)
+    got = [host(x) for x in c.run(B)]
+    for x, y in zip(got, clean):
+        assert np.array_equal(x[:new - 1], y[:new - 1]) and np.array_equal(x[new:], y[new:])
+        assert np.isnan(x[new - 1]).all()
+
+
+@pytest.mark.parametrize("lens", [[90, 33], [1700, 200]])
+def test_values_whose_sums_overflow(B, lens):
+    """V up to bf16's largest: their mean is finite, their sum is not."""
+    c = Case(lens, 1, 4, 64, 16, 18, 2)
+    clean = [host(x) for x in c.run(B)]
+    c.v = bf16_round(np.sign(c.v) * np.minimum(np.abs(c.v), 1.0) * np.float32(3.38e38))
+    c.v[..., :7] = np.float32(3.38e38)
+    c.v = bf16_round(c.v)
+    announce("attention over large values", lens)
+    got = c.run(B)
+    c.check(got)
+    assert np.isfinite(host(got[0])).all() and np.array_equal(host(got[1]), clean[1])
+
+
 def test_infinite_values_that_are_seen(B):
     """An infinity in V makes its dimension infinite, of its sign, for the rows
     that see it; infinities of both signs make NaN; others keep their bits."""
