@@ -610,12 +610,14 @@ int64_t attention_workspace(int64_t seqs, int64_t capacity, int q_heads, int hea
   return n == 1 ? 0 : seqs * n_new * q_heads * n * (hd + 2) * 4;
 }
 
-// As many workgroups as the chip holds at once (by their registers), if there is
-// a chunk for each wave: one that starts later starts its loads from nothing.
+// As many workgroups as the chip holds at once (by their registers), or one for
+// each chunk, whose waves then lie on as many compute units as they can (96
+// chunks: 10.4 us, in a quarter of the workgroups 11.6).  A workgroup that starts
+// later would start its loads from nothing.
 template <int HB, bool E4M3, int RT>
 static void attend(const AttendArgs& a, const Split& sp, int64_t most, int cus, hipStream_t stream) {
   constexpr int kHeld = HB * RT <= 2 ? 3 : HB <= (RT == 1 ? 4 : 2) ? 2 : 1;
-  const int grid = (int)std::min<int64_t>((most + 3) / 4, (int64_t)cus * kHeld);
+  const int grid = (int)std::min<int64_t>(most, (int64_t)cus * kHeld);
   cache_attention_kernel<HB, E4M3, RT><<<grid, 256, 0, stream>>>(a, sp);
 }
 

@@ -71,13 +71,17 @@ struct Span {
   int len, first, start, chunk, n;   // first key seen; start: first rounded down to a tile
 };
 
-// The least chunk is one block, or two where the sequence alone makes more than
-// 128 chunks over its heads.  One sequence of 1,021 tokens over 12 heads of 64
-// takes 11.4 us with one and 14.8 with two; 64 sequences of up to 8,192 over 4
-// heads of 256 take 237 us and 10 to join with one, 225 and 7 with two (half as
-// many sums are written and read again).
+// The least chunk is one block, or two where one block makes more than 512 chunks
+// of the sequence's heads.  One sequence over 4 heads of 256 takes 18.7 us (and 5
+// to join) for 8,000 tokens with one block, 38.1 with two; 32 sequences of up to
+// 4,096 tokens over 8 heads of 128, 5 new ones each, 85 and 12.8 with one, 82 and
+// 10.7 with two (half as many sums are written and read again).  Half a block
+// would take 9.4 us instead of 10.4 for 1,021 tokens over 12 heads of 64, but
+// 256 instead of 237 for 64 sequences of up to 8,192 over 4 heads of 256.
+constexpr int64_t kFine = 512 * kBlock;      // keys times heads
+
 __host__ __device__ inline int least_chunk(int64_t keys, int heads) {
-  return keys * heads <= 128 * kBlock ? kBlock : 2 * kBlock;
+  return keys * heads <= kFine ? kBlock : 2 * kBlock;
 }
 
 __host__ __device__ inline Span span_of(int len, int n_new, int window, int heads) {
@@ -103,7 +107,7 @@ inline int most_chunks(int64_t capacity, int n_new, int window, int heads) {
     const int64_t seen = (int64_t)window + n_new - 1 + kTile - 1;
     keys = keys < seen ? keys : seen;
   }
-  const int64_t most = 128 * kBlock / heads, small = keys < most ? keys : most;
+  const int64_t most = kFine / heads, small = keys < most ? keys : most;
   const int64_t least = least_chunk(keys, heads);
   int64_t n = (keys + least - 1) / least;
   if ((small + kBlock - 1) / kBlock > n) n = (small + kBlock - 1) / kBlock;
