@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
     ++t.seq;
     if (t.seq < cv.seqs) t.span = span_here(a, t.seq);
   };
-  // The block that comes after the one at work: its item, how many items come
-  // after that (-1: there is no such block), its first key.
+  // A block ahead of the one at work (two, from the last tile of it on): its item,
+  // how many items come after that (-1: there is no such block), its first key.
   Item soon;
   int soon_after, soon_k0;
   auto soon_from = [&]() {                                 // on to an item that has keys
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
   int64_t soon_head = 0;                                   // the byte offset of its head
   auto put_places = [&](int64_t* to) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    asm volatile("" : "+v"(pages[0]), "+v"(pages[1]));     // not looked at before this place
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int key = soon_k0 + i * 64 + lane;
@@ -253,6 +254,12 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     soon_head = soon_after >= 0 ? (soon.part % cv.heads) * cv.head_bytes : 0;
+    // the block after that: its pages are asked for before the tile's K, so they
+    // are there when a K is
+    soon_k0 += kBlock;
+    soon_from();
+    ask_pages();
+    __builtin_amdgcn_sched_barrier(0);
   };
   typedef std::conditional_t<E4M3, u32x2_t, u32x4_t> kword_t;   // eight values
   kword_t kw[2][HB];                                       // a tile on its way
@@ -349,9 +356,6 @@ __global__ void __launch_bounds__(256, HB <= (RT == 1 ? 4 : 2) ? 2 : 1) cache_at
       valid[0] = soon_valid[0];
       valid[1] = soon_valid[1];
       const int64_t block_head = soon_head;
-      soon_k0 += kBlock;
-      soon_from();
-      ask_pages();
       const int tiles = (min(hi - kb, kBlock) + kTile - 1) / kTile;
       for (int tile = 0; tile < tiles; ++tile) {
         const int k0 = kb + tile * kTile;
