@@ -1199,9 +1199,9 @@ class KvCache:
     [seqs, pages_per_seq], whose page t / page_size holds token t, a page
     outside the cache (-1) none; ``k_scale``, ``v_scale``: fp32 [heads] or
     None, what a stored value is to be multiplied by.  The tensors stay the
-    caller's; their contents may change between calls.
+    caller's; their contents may change between calls, their memory may not.
     """
-    __slots__ = ("k", "v", "page_table", "k_scale", "v_scale", "desc", "_at", "_workspace")
+    __slots__ = ("k", "v", "page_table", "k_scale", "v_scale", "desc", "_at", "_memory", "_workspace")
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
         torch = _torch()
@@ -1236,7 +1236,20 @@ class KvCache:
             page_table.stride(0) if seqs > 1 else per_seq, types[k.dtype], pages, page_size, heads,
             head_dim, seqs, per_seq)
         self._at = ctypes.addressof(self.desc)
+        self._memory = [(t, t.data_ptr()) for t in (k, v, page_table, k_scale, v_scale) if t is not None]
         self._workspace = {}
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "_workspace"):
+            raise AttributeError(f"{name}: a KvCache stays as it was made; make another")
+        object.__setattr__(self, name, value)
+
+    def _here(self) -> KvCacheDesc:
+        """The descriptor, whose addresses must still be the tensors'."""
+        for t, at in self._memory:
+            if t.data_ptr() != at:
+                raise ValueError("cache: one of its tensors has other memory than when it was made")
+        return self.desc
 
     def _attention_workspace(self, *sizes) -> int:
         n = self._workspace.get(sizes)
@@ -1263,7 +1276,7 @@ def ds_cache_append_rows(cache: KvCache, k, v, positions, seqs=None, inv_freq=No
     rotated, are returned (``q_out``, which may be q); None otherwise.
     """
     torch = _torch()
-    desc = cache.desc
+    desc = cache._here()
     heads, head_dim = desc.n_heads, desc.head_dim
     if head_dim <= 0:
         raise ValueError("cache: has no head_dim")
@@ -1317,7 +1330,7 @@ def ds_cache_attention_rows(cache: KvCache, q, lens, scale: Optional[float] = No
     with fp32 lse [rows, nq]; a row that sees nothing gets 0 and -infinity.
     """
     torch = _torch()
-    desc = cache.desc
+    desc = cache._here()
     head_dim, seqs = desc.head_dim, desc.n_seqs
     if head_dim <= 0:
         raise ValueError("cache: has no head_dim")

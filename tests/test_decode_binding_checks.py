@@ -102,3 +102,13 @@ def test_a_caches_description():
     assert (c.desc.ld_table, c.desc.pages_per_seq, c.desc.n_seqs, c.desc.page_size) == (9, 4, 3, 16)
     c = cache(k=z(1, 1, 1, 16, dtype=bf16), v=z(1, 1, 1, 16, dtype=bf16), page_table=z(1, 9, dtype=torch.int32)[:, :4])
     assert (c.desc.page_stride, c.desc.token_stride, c.desc.head_stride, c.desc.ld_table) == (0, 0, 0, 4)
+
+
+def test_a_cache_stays_as_it_was_made():
+    c = cache()
+    with pytest.raises(AttributeError, match="make another"):
+        c.k = c.v
+    c.page_table.set_(z(3, 4, dtype=torch.int32))                 # other memory under the same tensor
+    for f, a in (CALLS["append"], CALLS["attend"]):
+        with pytest.raises(ValueError, match="other memory"):
+            f(**{**a, "cache": c})
