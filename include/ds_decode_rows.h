@@ -197,8 +197,14 @@ int ds_cache_append_rows(const ds_kv_cache* cache, const uint16_t* q, int64_t ld
  * A row that sees nothing (t < 0, no page, every z_u -infinity) has out 0 and
  * lse -infinity.  What lies in the cache at tokens that a row does not see
  * (NaN and infinity too) does not reach it.
- * The probabilities are formed relative to the largest z so far and rounded
- * to two bf16 parts (16 bits) for the matrix instructions; sums are in fp32.
+ * The weights are formed relative to a maximum within log 2^8 of the largest z
+ * so far and rounded to two bf16 parts (16 bits) for the matrix instructions;
+ * sums are in fp32.  Rows whose sums are not finite (V holds an infinity or a
+ * NaN, or values whose sum overflows) are summed again one key at a time, which
+ * is right and slow.
+ *
+ * Where a sequence is cut for that goes by L, n_heads and, with a window, where
+ * its first row's window begins; by nothing else.
  *
  * q, out   : [rows, ldq] / [rows, ldout] bf16 bit patterns, the first
  *            n_q_heads * head_dim elements used, rows = n_seqs * new_tokens;

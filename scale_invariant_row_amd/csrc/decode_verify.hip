@@ -13,8 +13,8 @@
 // distribution at once: with weights known to 1e-7 and a vocabulary of 1e5,
 // about one choice in a thousand would fall on the other side of a border.
 // That makes it bound by the ALUs: 24 instructions an element, 12 of them fp64
-// (at fp32's rate), are 45 us of the first launch's 58 over 576 rows of 131,072
-// bf16 logits (151 MB), and 10 of the last's 33.
+// (at fp32's rate), are 45 us of the first launch's 59 over 576 rows of 131,072
+// bf16 logits (151 MB), and 10 of the last's 32.
 #include "decode_launch.hpp"
 #include "row_kernels.hpp"
 

@@ -218,6 +218,45 @@ def test_infinite_values_that_are_seen(B):
     assert (np.abs(got[0] - want)[fine] <= (rel * mag + 2.0 ** -8 * np.abs(want))[fine]).all()
 
 
+@pytest.mark.parametrize("kind,new,group,window", [("e4m3", 1, 3, 0), ("e4m3", 5, 6, 200), ("bf16", 2, 9, 333)])
+def test_a_nan_in_a_seen_value_is_its_dimensions(B, kind, new, group, window):
+    """... for the rows that see it, over several chunks and tiles."""
+    c = Case([700, 150], 2, group, 80, 16, 19, new, window, kind)
+    for t in (600, 690, 699):
+        c.v[D.token_place(c.table, c.n_pages, 16, 0, t)][..., t % 80] = np.nan
+    announce("attention over a NaN in V", kind, new, group, window)
+    got = c.run(B)
+    with np.errstate(invalid="ignore"):
+        want = D.attention(c.q, c.k, c.v, c.table, c.lens, new, c.nq, window, c.scale, *c.scales)[0]
+    assert np.array_equal(np.isnan(host(got[0])), np.isnan(want)) and np.isnan(want).any() and not np.isnan(want).all()
+    out, lse = c.check(got)
+    assert np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_lse_of_one_score_is_rounded_twice(B, kind):
+    """One product a score and one token a row: z is off by the rounding of z
+    log2 e (1 unit of 2^-24 of it), the result by its own (1)."""
+    c = Case([1] * 60, 2, 4, 64, 16, 21, kind=kind)
+    rng = np.random.default_rng(22)
+    q = np.zeros((60, 8, 64), np.float32)
+    at = rng.integers(0, 64, (60, 8))
+    np.put_along_axis(q, at[..., None], bf16_round(rng.standard_normal((60, 8, 1)) * 9), 2)
+    c.q, c.scale = q.reshape(60, 512), 0.1171875 * 1.1
+    announce("lse of single scores", kind)
+    got = host(c.run(B)[1])
+    c.check(c.run(B))
+    lse = D.attention(c.q, c.k, c.v, c.table, c.lens, 1, 8, 0, c.scale, *c.scales)[1]
+    assert (np.abs(got - lse) <= 2.001 * U * np.abs(lse) + 1e-30).all()
+
+
+def test_many_empty_sequences(B):
+    c = Case([0] * 1500 + [70] + [0] * 37, 1, 2, 32, 16, 20, 1)
+    announce("attention of 1,537 sequences and hardly a token")
+    out, lse = c.check(c.run(B))
+    assert not out[:1500].any() and out[1500].any() and (lse[1501:] == -np.inf).all()
+
+
 def test_scores_that_are_all_minus_infinity(B):
     """Keys of -infinity (a mask written into the cache) leave nothing; some do
     not matter beside others; a scale of 0 gives the mean."""
