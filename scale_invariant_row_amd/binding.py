@@ -1231,6 +1231,8 @@ class KvCache:
                 raise ValueError(f"{n}: must be on the device of k")
         self.k, self.v, self.page_table, self.k_scale, self.v_scale = k, v, page_table, k_scale, v_scale
         seqs, per_seq = page_table.shape
+        if max(pages, page_size, heads, head_dim, seqs, per_seq) >= 1 << 31:
+            raise ValueError("cache: a dimension of 2^31 or more")
         self.desc = KvCacheDesc(
             k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), page_table.data_ptr(), *strides,
             page_table.stride(0) if seqs > 1 else per_seq, types[k.dtype], pages, page_size, heads,

@@ -93,6 +93,14 @@ def test_bad_cache_is_named(over, word):
         cache(**over)
 
 
+def test_a_dimension_past_32_bits_is_refused():
+    wide = z(1, 1, 1, 16, dtype=bf16).expand((1 << 32) + 1, 1, 1, 16)
+    with pytest.raises(ValueError, match="2\\^31"):
+        cache(k=wide, v=wide)
+    with pytest.raises(ValueError, match="2\\^31"):
+        cache(page_table=z(1, 4, dtype=torch.int32).expand((1 << 32) + 3, 4))
+
+
 def test_a_caches_description():
     c = cache()
     assert (c.desc.page_stride, c.desc.token_stride, c.desc.head_stride) == (16 * HEADS * HD, HEADS * HD, HD)
