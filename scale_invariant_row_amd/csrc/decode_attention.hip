@@ -98,24 +98,40 @@ struct Item {
 
 // The number of chunks (of one part) of sequence s0 + lane, 0 past the last.
 __device__ __forceinline__ int chunks_of(const AttendArgs& a, int s0, int lane) {
-  if (s0 + lane >= a.cache.seqs) return 0;
-  const int len = a.lens[s0 + lane], cap = a.cache.pages_per_seq << a.cache.page_shift;
-  return span_of(len < 0 ? 0 : len > cap ? cap : len, a.n_new, a.window, a.cache.heads).n;
+  const int last = a.cache.seqs - 1, cap = a.cache.pages_per_seq << a.cache.page_shift;
+  const int len = a.lens[min(s0 + lane, last)];
+  const int n = span_of(len < 0 ? 0 : len > cap ? cap : len, a.n_new, a.window, a.cache.heads).n;
+  return s0 + lane > last ? 0 : n;
+}
+
+// And of the N * 64 sequences from s0 on together, their lengths asked for at once.
+template <int N>
+__device__ __forceinline__ int chunks_from(const AttendArgs& a, int s0, int lane) {
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum += chunks_of(a, s0 + i * 64, lane);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  return __builtin_amdgcn_readfirstlane(sum);
 }
 
 __device__ __forceinline__ int64_t list_length(const AttendArgs& a, int parts, int lane) {
+  if (a.cache.seqs <= 64) return (int64_t)chunks_from<1>(a, 0, lane) * parts;
   int sum = 0;
-  for (int s0 = 0; s0 < a.cache.seqs; s0 += 64) sum += chunks_of(a, s0, lane);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-  return (int64_t)__builtin_amdgcn_readfirstlane(sum) * parts;
+  for (int s0 = 0; s0 < a.cache.seqs; s0 += 512) sum += chunks_from<8>(a, s0, lane);
+  return (int64_t)sum * parts;
 }
 
 // The item at place `at` of the list.
 __device__ __forceinline__ Item item_at(const AttendArgs& a, int parts, int64_t at, int lane) {
   Item it{0, 0, 0, {}};
-  int before = 0;                                          // chunks of the sequences before these 64
-  for (int s0 = 0; s0 < a.cache.seqs; s0 += 64) {
+  int before = 0, s0 = 0;                                  // chunks of the sequences before s0
+  for (; s0 + 64 < a.cache.seqs; s0 += 512) {
+    const int sum = chunks_from<8>(a, s0, lane);
+    if (at < (int64_t)(before + sum) * parts) break;
+    before += sum;
+  }
+  for (; s0 < a.cache.seqs; s0 += 64) {
     const int n = chunks_of(a, s0, lane);
     int upto = n;
 #pragma unroll
