@@ -198,8 +198,8 @@ int ds_cache_append_rows(const ds_kv_cache* cache, const uint16_t* q, int64_t ld
  * lse -infinity.  What lies in the cache at tokens that a row does not see
  * (NaN and infinity too) does not reach it.
  * The weights are formed relative to a maximum within log 2^8 of the largest z
- * so far and rounded to two bf16 parts (16 bits) for the matrix instructions;
- * sums are in fp32.  Rows whose sums are not finite (V holds an infinity or a
+ * so far and go into the matrix instructions as three bf16 parts, which hold
+ * all their 24 bits; sums are in fp32.  Rows whose sums are not finite (V holds an infinity or a
  * NaN, or values whose sum overflows) are summed again one key at a time, which
  * is right and slow.
  *
