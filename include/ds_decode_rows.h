@@ -231,7 +231,8 @@ int64_t ds_cache_attention_rows_workspace(const ds_kv_cache* cache, int32_t n_q_
  * given random numbers.
  *
  * Sequence s has n_drafts + 1 rows of target logits and n_drafts rows of draft
- * logits.  In fp64, from z = x * scale * inv_temp (fp32 products in this order):
+ * logits.  In fp64, from z = x * scale * inv_temp (fp32 products in this order),
+ * with exp(-d) off by at most (2 + d / 3) 2^-53 of itself:
  *   p_i = softmax of target row s * (n_drafts + 1) + i
  *   q_i = softmax of draft row s * n_drafts + i; without draft logits, 1 at
  *         the drafted token d_i and 0 elsewhere

@@ -12,10 +12,11 @@
 // fp64, because a token's choice hangs on every border of the cumulated
 // distribution at once: with weights known to 1e-7 and a vocabulary of 1e5,
 // about one choice in a thousand would fall on the other side of a border.
-// That makes it bound by the ALUs: 24 instructions an element, 12 of them fp64
-// (at fp32's rate), are 45 us of the first launch's 59 over 576 rows of 131,072
+// That makes it bound by the ALUs: 25 instructions an element, 13 of them fp64
+// (at fp32's rate), are 47 us of the first launch's 61 over 576 rows of 131,072
 // bf16 logits (151 MB), and 10 of the last's 32.
 #include "decode_launch.hpp"
+#include "powers_of_two.hpp"
 #include "row_kernels.hpp"
 
 namespace dsr {
@@ -111,26 +112,32 @@ __device__ __forceinline__ void load_logits(const VerifyArgs& a, int which, int6
   }
 }
 
-// exp: 2^(k / 128) from a table in LDS times a cubic, off by at most 3e-12 of
-// itself (the quartic term at half a step, (ln 2 / 256)^4 / 24).  12 fp64
-// instructions; the library's takes three times as long.
+// exp to fp64's precision: with k ln 2 / 256 next to d and r what is left of d,
+// 2^(k / 256) from a table in LDS times exp(r) to its fourth power.  Off by at most
+// (2 + |d| / 3) 2^-53 of itself: half a unit each for the table and the last
+// rounding, 0.4 for the fifth power at half a step, (ln 2 / 512)^5 / 120, and 0.3 |d|
+// for ln 2 / 256 in one part.  13 fp64 instructions an element, a sum among them; a
+// table of 128 and a cubic, 12, are 2.2e-12 off and take as long.
 struct ExpTable {
-  double t[128];
-  __device__ __forceinline__ void fill() {               // by 128 threads at least; a barrier follows
-    if (threadIdx.x < 128) t[threadIdx.x] = exp2((double)threadIdx.x * 0x1p-7);
+  double t[256];
+  __device__ __forceinline__ void fill() {               // by 256 threads at least; a barrier follows
+    if (threadIdx.x < 256) t[threadIdx.x] = kPowersOfTwo[threadIdx.x];
   }
   // exp(z - m) for z <= m, m finite
   __device__ __forceinline__ double operator()(float z, float m) const {
-    constexpr double kPer = 184.66496523378731;          // 128 / ln 2
-    constexpr double kA = 0.0054152123481245727;         // ln 2 / 128
+    constexpr double kPer = 369.3299304675746;           // 256 / ln 2
+    constexpr double kStep = 0.0027076061740622863;      // ln 2 / 256
     constexpr double kMagic = 6755399441055744.0;        // 1.5 * 2^52: the sum's low bits are the whole number
     const double d = fmax((double)z - (double)m, -800.0);   // exp(-800) is 0, and so is a masked token's
     const double y = __builtin_fma(d, kPer, kMagic);
-    const double r = __builtin_fma(d, kPer, kMagic - y);
+    const double r = __builtin_fma(kMagic - y, kStep, d);
     const int k = (int)__builtin_bit_cast(int64_t, y);
-    double v = __builtin_fma(__builtin_fma(kA * kA * kA / 6.0, r, kA * kA / 2.0), r, kA);
-    v = __builtin_fma(v, r, 1.0) * t[k & 127];
-    return __builtin_amdgcn_ldexp(v, k >> 7);
+    double v = __builtin_fma(r, 1.0 / 24.0, 1.0 / 6.0);
+    v = __builtin_fma(v, r, 0.5);
+    v = __builtin_fma(v, r, 1.0);
+    const double from = t[k & 255];
+    v = __builtin_fma(from, v * r, from);
+    return __builtin_amdgcn_ldexp(v, k >> 8);
   }
 };
 
