@@ -357,7 +357,8 @@ __device__ __forceinline__ Place find_part(const double* of, int n, double u, in
       if (i * 64 < n) total[k] += wave_sum_f64(w[k][i]);
     }
   Place at{-1, !(total[0] > 0.0), 0.0};                    // p = q: nothing is left over
-  const double edge = u * total[at.whole];
+  // at or above 1, or NaN: past every sum, whose order may bring one to the total early
+  const double edge = u < 1.0 ? u * total[at.whole] : __builtin_inf();
   double before = 0.0;
 #pragma unroll
   for (int i = 0; i < kMaxParts / 64; ++i) {
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const VerifyA
   if (!is_last) return;
   if (wave == 0) {
     const double u = (double)a.u_sample[seq];
-    const Place at = find_part(of, n_parts, u < 0.0 ? 0.0 : u, lane);   // (a NaN stays one)
+    const Place at = find_part(of, n_parts, u < 0.0 ? 0.0 : u, lane);
     if (lane == 0) place = at;
   }
   __syncthreads();

@@ -65,3 +65,21 @@ def test_a_sample_near_its_border(B, seed):
                                  torch.empty(n, 0, device="cuda:0"), dev(u))
     torch.cuda.synchronize()
     assert np.array_equal(host(got.tokens)[:, 0] == 0, first)
+
+
+@pytest.mark.parametrize("vocab", [4096, 700, 10001])
+@pytest.mark.parametrize("u", [1.0, 1.5, np.inf, np.nan])
+def test_random_numbers_past_the_range_give_the_last_token(B, vocab, u):
+    """Rows whose upper half has weights under fp64's rounding of their total: the
+    running sum is at the total long before the last token."""
+    import torch
+    rng = np.random.default_rng(vocab)
+    z = rng.standard_normal((200, vocab)).astype(np.float32)
+    z[:, vocab // 2:] -= 60
+    z[100:, -5:] = -np.inf
+    announce("sample past the range", vocab, u)
+    got = B.ds_draft_verify_rows(dev(z), torch.empty(200, 0, dtype=torch.int32, device="cuda:0"),
+                                 torch.empty(200, 0, device="cuda:0"), dev(np.full(200, u, np.float32)))
+    torch.cuda.synchronize()
+    want = np.where(np.arange(200) < 100, vocab - 1, vocab - 6)
+    assert np.array_equal(host(got.tokens)[:, 0], want)
