@@ -157,7 +157,7 @@ def verify_sequence(target, draft, drafted, u_accept, u_sample):
         edge = float(u_accept[i]) * q[d]
         if edge > 0 or pd > 0:
             margin = min(margin, abs(edge - pd) / max(edge, pd))
-        if not edge < pd:
+        if p is None or not edge < pd:
             weight = np.zeros(vocab) if p is None else np.maximum(p - q, 0)
             if p is not None and not weight.any():
                 weight = p

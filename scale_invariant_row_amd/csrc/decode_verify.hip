@@ -281,7 +281,7 @@ __device__ __forceinline__ Choice decide(const VerifyArgs& a, const Slice* slice
         says = q.sum > 0.0;
         if (says) qd = table(zq, q.m) / q.sum;
       }
-      ok = says && (double)u * qd < pd;
+      ok = says && p.sum > 0.0 && (double)u * qd < pd;     // (a u below 0 is below p = 0 too)
     }
     const uint64_t stops = __builtin_amdgcn_ballot_w64(!ok);   // (lanes past the drafts stop)
     const int first = __builtin_ctzll(stops);

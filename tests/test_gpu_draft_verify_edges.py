@@ -83,3 +83,21 @@ def test_random_numbers_past_the_range_give_the_last_token(B, vocab, u):
     torch.cuda.synchronize()
     want = np.where(np.arange(200) < 100, vocab - 1, vocab - 6)
     assert np.array_equal(host(got.tokens)[:, 0], want)
+
+
+@pytest.mark.parametrize("certain", [False, True])
+def test_target_rows_that_say_nothing_refuse_whatever_the_random_number(B, certain):
+    """Below 0 it is below a probability of 0 too."""
+    from test_gpu_draft_verify import Case
+    c = Case(8, 2, 300, 40, certain=certain)
+    c.target[0, 0] = -np.inf
+    c.target[1, 0, 7] = np.nan
+    c.target[2, 1] = -np.inf
+    c.target[3, 1, 9] = np.inf
+    c.ua[:4] = -0.5
+    c.ua[4] = -1e-30
+    announce("verify with random numbers below 0", certain)
+    got = c.run(B)
+    c.check(got)
+    assert host(got.accepted)[:5].tolist() == [0, 0, 1, 1, 2]
+    assert host(got.tokens)[:2, 0].tolist() == [-1, -1] and np.isfinite(host(got.logp)).all()
