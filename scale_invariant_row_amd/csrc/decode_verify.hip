@@ -449,11 +449,13 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const VerifyA
       __hip_atomic_store(of + here * 2 + k, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     // The sums are stored past this die's caches, and waited for, before the count
-    // is added to: who counts last reads them all, past its own caches.  (An
-    // atomic that releases and acquires whole caches took 44 us where this
-    // takes 34.)
-    __builtin_amdgcn_s_waitcnt(0);
-    asm volatile("" ::: "memory");
+    // is added to: who counts last reads them all, past its own caches.  That order
+    // is this chip's, not the memory model's, to which relaxed accesses of two places
+    // have none: a store of agent scope is counted until it lies where every die reads
+    // it.  The wait is an instruction that no access may be moved across, so the source
+    // alone keeps it.  (An atomic that releases and acquires whole caches, which the
+    // model would ask for, took 44 us where this takes 34.)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     is_last = __hip_atomic_fetch_add(done + seq, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)n_parts - 1;
   }
   __syncthreads();
