@@ -1183,7 +1183,7 @@ def ds_rope_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 
     """
     torch = _torch()
     rotary_dim = int(rotary_dim)
-    f = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.float32)
+    f = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.float32, device="cpu")
     _check(_decode_lib().ds_rope_frequencies(f.data_ptr(), rotary_dim, base, factor, original, low,
                                              high), "ds_rope_frequencies")
     return f if device is None else f.to(device)
