@@ -1295,7 +1295,7 @@ def ds_cache_append_rows(cache: KvCache, k, v, positions, seqs=None, inv_freq=No
         raise ValueError("q_out: expected q's heads")
     _vec(positions, "positions", rows, torch.int32)
     _vec(seqs, "seqs", rows, torch.int32)
-    if seqs is None and (desc.n_seqs == 0 or rows % desc.n_seqs):
+    if seqs is None and rows and (desc.n_seqs == 0 or rows % desc.n_seqs):
         raise ValueError(f"seqs: needed, {rows} rows are no multiple of {desc.n_seqs} sequences")
     if inv_freq is not None:
         _frequencies(inv_freq, head_dim)
