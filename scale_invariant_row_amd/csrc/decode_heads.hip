@@ -222,9 +222,15 @@ __device__ __forceinline__ float over_scale(float x, float scale, float inv) {
 // Eight values as e4m3: to nearest even, the largest past its range, NaN kept.
 __device__ __forceinline__ u32x2_t pack8_e4m3(const float* v, float scale, float inv) {
   float q[8];
+  if (inv != 0.f && fabsf(inv) < __builtin_inff()) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = over_scale(v[j], scale, inv);
+  } else {                                   // a scale below 2^-128 or infinite: 1 / scale says nothing of it
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = v[j] / scale;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    q[j] = over_scale(v[j], scale, inv);
     q[j] = q[j] > 448.f ? 448.f : q[j] < -448.f ? -448.f : q[j];
   }
   int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
