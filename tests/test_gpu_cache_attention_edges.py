@@ -53,3 +53,27 @@ def test_weights_keep_the_bits_of_fp32(B, kind, group):
     got = c.run(B)
     out, _ = c.check(got)
     near(host(got[0]), out, 19 * U)
+
+
+def test_a_tiny_scale_of_values_costs_no_bits(B):
+    """Two tokens a sequence as above, w v times a scale of 1e-40: in units of 2^-24
+    at most 19, and 1 for one product more.  The scale over 1 + w has 16 bits."""
+    rng = np.random.default_rng(32)
+    heads, group, hd, seqs = 4, 4, 64, 60
+    c = Case([2] * seqs, heads, group, hd, 16, 33, kind="e4m3")
+    c.scale = 1.0
+    c.scales = np.ones(heads, np.float32), np.full(heads, 1e-40, np.float32)
+    c.k[:], c.v[:] = 0, 0
+    for s in range(seqs):
+        page, off = D.token_place(c.table, c.n_pages, 16, s, 1)
+        c.k[page, off, :, 0] = 0.125 * rng.integers(1, 9, heads)
+        c.v[page, off] = (8 + rng.integers(0, 7, (heads, hd))) * 32.0  # 256 to 448
+    q = np.zeros((seqs, heads * group, hd))
+    q[:, :, 0] = -rng.uniform(0.0, 0.5, (seqs, heads * group))
+    c.q = bf16_round(q.reshape(seqs, -1))
+    announce("attention of values of a tiny scale")
+    out = D.attention(c.q, c.k, c.v, c.table, c.lens, 1, c.nq, 0, c.scale, *c.scales)[0]
+    fine = out > 2.0 ** -126                                      # (bf16 has fewer bits below)
+    assert fine.mean() > 0.5
+    got = host(c.run(B)[0])
+    near(got[fine], out[fine], 20 * U)
