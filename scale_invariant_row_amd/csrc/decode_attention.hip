@@ -646,7 +646,8 @@ __global__ void __launch_bounds__(256) cache_attention_join_kernel(const AttendA
   __syncthreads();
   if (wave != 0 || d >= hd) return;
   for (int w = 1; w < 4; ++w) s += *(const f32x4_t*)(part[w] + d);
-  const float v_scale = a.cache.v_scale != nullptr ? a.cache.v_scale[qh / (a.q_heads / a.cache.heads)] : 1.f;
+  const float v_scale = sum == 0.f ? 0.f                   // (0 times an infinite scale)
+                        : a.cache.v_scale != nullptr ? a.cache.v_scale[qh / (a.q_heads / a.cache.heads)] : 1.f;
   *(u32x2_t*)(a.out + row * a.ldo + (int64_t)qh * hd + d) =
       u32x2_t{pack_bf16(s.x * v_scale, s.y * v_scale), pack_bf16(s.z * v_scale, s.w * v_scale)};
   if (lane == 0 && a.lse != nullptr) {

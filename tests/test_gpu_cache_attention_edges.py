@@ -77,3 +77,14 @@ def test_a_tiny_scale_of_values_costs_no_bits(B):
     assert fine.mean() > 0.5
     got = host(c.run(B)[0])
     near(got[fine], out[fine], 20 * U)
+
+
+@pytest.mark.parametrize("scale", [np.inf, np.nan])
+def test_rows_that_see_nothing_are_zeros_under_any_scale(B, scale):
+    """Of one chunk, of several, and of a length without pages."""
+    c = Case([0, 40, 700, 300], 2, 4, 64, 16, 34, kind="e4m3")
+    c.table[1:3] = -1
+    c.scales = tuple(np.full(2, scale, np.float32) for _ in "kv")
+    announce("attention of nothing under a scale of", scale)
+    out, lse = (host(x) for x in c.run(B))
+    assert not out[:3].any() and (lse[:3] == -np.inf).all() and np.isnan(out[3]).all()
