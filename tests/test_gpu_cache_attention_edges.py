@@ -1,6 +1,9 @@
-"""ds_cache_attention_rows on the GPU where its numerics have edges, against the
-float64 oracle: what the weights keep, beside the cases of
-test_gpu_cache_attention.py.
+"""ds_cache_attention_rows on the GPU where its numerics and its cuts have edges,
+against the float64 oracle, beside the cases of test_gpu_cache_attention.py.
+
+Bounds as there, without the 2^-16 that weights of 16 bits would leave: z off by
+E = 2^-24 (2 hd + 12) S, a weight by 2 E + 2^-24 (n + 96), out by sum p |v| times
+(2 E + 2^-24 (2 n + 96)).
 """
 import numpy as np
 import pytest
@@ -8,7 +11,7 @@ import pytest
 from gpu_util import announce
 from oracle import decode_rows as D
 from test_gpu_cache_attention import Case
-from token_util import U, bf16_round, host
+from token_util import U, bf16_round, close, host
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +91,59 @@ def test_rows_that_see_nothing_are_zeros_under_any_scale(B, scale):
     announce("attention of nothing under a scale of", scale)
     out, lse = (host(x) for x in c.run(B))
     assert not out[:3].any() and (lse[:3] == -np.inf).all() and np.isnan(out[3]).all()
+
+
+def check(c, got):
+    out, lse, mag, big, seen = D.attention(c.q, c.k, c.v, c.table, c.lens, c.new, c.nq, c.window, c.scale, *c.scales)
+    E, n = U * (2 * c.hd + 12) * big, seen[:, None]
+    close(host(got[1]), lse, E + U * (n + 96 + 4 * np.abs(np.where(np.isfinite(lse), lse, 0))), "lse")
+    rel = np.repeat(2 * E + U * (2 * n + 96), c.hd, axis=1)
+    with np.errstate(invalid="ignore"):
+        fine = np.isfinite(out)
+        close(np.where(fine, host(got[0]), 0), np.where(fine, out, 0), np.where(fine, rel * mag, 0), "out", bf16=True)
+    return out
+
+
+# kv heads, lengths: keys times heads about 65,536, where a least chunk goes from
+# 128 keys to 256, and about 128 chunks of either, past which chunks hold more
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,window", [(1, 0), (3, 0), (2, 8192), (5, 8189)])
+@pytest.mark.parametrize("heads,lens", [(8, [8191, 8192, 8193, 5]), (8, [33000, 8190, 32767, 32769]),
+                                        (4, [16383, 16384, 16385, 16400]), (3, [21845, 21846, 300])])
+def test_where_the_cut_changes(B, heads, lens, new, window, kind):
+    c = Case(lens, heads, 2, 32, 64, 35 + heads, new, window, kind)
+    announce("attention where the cut changes", heads, lens, new, window, kind)
+    got = c.run(B)
+    check(c, got)
+    for s in (0, len(lens) - 1):                                  # alone, under its own table: the same bits
+        one = Case([lens[s]], heads, 2, 32, 64, 1, new, window, kind)
+        per = one.table.shape[1]
+        one.k, one.v, one.scales, one.q = c.k, c.v, c.scales, c.q[s * new:(s + 1) * new]
+        one.table, one.n_pages = c.table[s:s + 1, :per], c.n_pages
+        for x, y in zip(one.run(B), got):
+            assert np.array_equal(host(x), host(y)[s * new:(s + 1) * new])
+
+
+@pytest.mark.parametrize("lens", [[300, 90], [1700, 1100]])
+def test_rows_beside_infinite_values_are_as_exact_as_others(B, lens):
+    """They are summed again by themselves, one key at a time, in fp32."""
+    c = Case(lens, 1, 4, 64, 16, 36, 2)
+    at = lambda s, t: D.token_place(c.table, c.n_pages, 16, s, t)  # noqa: E731
+    c.v[at(0, 7)][..., 3] = np.inf
+    c.v[at(0, lens[0] - 20)][..., 5] = -np.inf
+    c.v[at(0, lens[0] - 1)][..., 9] = np.inf                      # the newest: its own row alone
+    c.v[at(0, 20)][..., 11], c.v[at(0, 21)][..., 11] = np.inf, -np.inf
+    announce("attention beside infinite values", lens)
+    got = c.run(B)
+    out = check(c, got)
+    assert np.array_equal(np.isfinite(host(got[0])), np.isfinite(out)) and not np.isfinite(out[:2]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group,new", [(7, 5), (3, 11), (16, 3), (5, 16), (40, 1)])
+def test_rows_of_several_groups(B, group, new, kind):
+    """33 to 80 rows a kv head: two or three groups of two row tiles, the last of
+    them not full."""
+    c = Case([1500, 40, 0, 300], 2, group, 64, 16, 37 + group, new, kind=kind)
+    announce("attention of rows of several groups", group, new, kind)
+    check(c, c.run(B))
