@@ -569,14 +569,19 @@ __global__ void __launch_bounds__(256, HB * RT <= 2 ? 3 : HB <= (RT == 1 ? 4 : 2
       if (at_row[r] < 0) continue;
       const bool mine = ((alone[r] >> col) & 1u) == 0;
       if (span.n == 1) {
-        // (v's scale apart: its quotient by l may have few bits left where it is tiny)
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r], vs = l[r] == 0.f ? 0.f : v_scale;
+        float inv = l[r] == 0.f ? 0.f : v_scale / l[r];
+        if (fabsf(v_scale) < 0x1p-64f) {                   // (uniform) few bits may be left of the quotient
+          const float share = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+          for (int d = 0; d < DB; ++d) o[r][d] *= share;
+          inv = v_scale;
+        }
         uint16_t* to = a.out + at_row[r] / a.q_heads * a.ldo + at_row[r] % a.q_heads * hd + grp * 4;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
           if (mine && d * 16 < hd)
-            *(u32x2_t*)(to + d * 16) = u32x2_t{pack_bf16(o[r][d].x * inv * vs, o[r][d].y * inv * vs),
-                                               pack_bf16(o[r][d].z * inv * vs, o[r][d].w * inv * vs)};
+            *(u32x2_t*)(to + d * 16) = u32x2_t{pack_bf16(o[r][d].x * inv, o[r][d].y * inv),
+                                               pack_bf16(o[r][d].z * inv, o[r][d].w * inv)};
         if (grp == 0 && a.lse != nullptr) a.lse[at_row[r]] = lse_of(m[r], l[r], (double)a.scale * k_scale, z_scale);
       } else {
         const int64_t part_at = (int64_t)at_row[r] * sp.max_chunks + item.c;
