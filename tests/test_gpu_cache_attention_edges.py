@@ -147,3 +147,29 @@ def test_rows_of_several_groups(B, group, new, kind):
     c = Case([1500, 40, 0, 300], 2, group, 64, 16, 37 + group, new, kind=kind)
     announce("attention of rows of several groups", group, new, kind)
     check(c, c.run(B))
+
+
+@pytest.mark.parametrize("kind,group,new,window", [("bf16", 4, 5, 0), ("e4m3", 4, 5, 0), ("bf16", 7, 5, 0), ("bf16", 3, 16, 0),
+                                                   ("e4m3", 40, 2, 0)])
+def test_a_newest_token_alone_has_the_same_bits(B, kind, group, new, window):
+    """In one row tile, among several tokens in two, and in several groups."""
+    lens = [700, 90, 33]
+    c = Case(lens, 2, group, 96, 16, 38, new, window, kind)
+    announce("attention of a newest token alone", kind, group, new)
+    whole = [host(x) for x in c.run(B)]
+    c.q, c.new = c.q.reshape(3, new, -1)[:, -1].copy(), 1
+    for x, y in zip(c.run(B), whole):
+        assert np.array_equal(host(x), y.reshape(3, new, -1)[:, -1])
+
+
+def test_values_below_the_normal_range(B):
+    """bf16 values under 2^-126 count as what they are, in one chunk and several."""
+    c = Case([40, 600], 1, 4, 64, 16, 39)
+    c.v = np.float32(2.0 ** -130) * np.clip(np.round(c.v * 2), -8, 8)
+    announce("attention of values below the normal range")
+    out, lse, mag, big, seen = D.attention(c.q, c.k, c.v, c.table, c.lens, 1, 4, 0, c.scale)
+    got = host(c.run(B)[0]).astype(np.float64)
+    bound = np.repeat(2 * U * (2 * 64 + 12) * big + U * (2 * seen[:, None] + 96), 64, axis=1) * mag
+    # fp32's step below its normal range is 2^-149, bf16's 2^-133: half of that one, and
+    # half of the other for each of a key's three products, with room for their join
+    assert (np.abs(got - out) <= bound + 2.0 ** -134 + 2 * 600 * 2.0 ** -149).all()
