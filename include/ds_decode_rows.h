@@ -214,7 +214,13 @@ int ds_cache_append_rows(const ds_kv_cache* cache, const uint16_t* q, int64_t ld
  *            included; below 0 counts as 0.
  * new_tokens : 1 <= new_tokens <= DS_MAX_NEW.  window >= 0.  scale: finite.
  * lse      : [rows, n_q_heads] fp32, or NULL.
- * workspace: of the size ds_cache_attention_rows_workspace returns.
+ * workspace: of the size ds_cache_attention_rows_workspace returns: head_dim + 2
+ *            floats for each chunk that a row's head may make by the table's
+ *            capacity (pages_per_seq * page_size, or the window), at most 128,
+ *            whatever the lengths are; 0 where that is one.  1,024 sequences of 32
+ *            q over 8 kv heads of 128 and up to 131,072 tokens: 2.2 GB.  A cache
+ *            described with the first columns of the same table, as many as the
+ *            longest sequence needs, takes less and gives the same bits.
  */
 int ds_cache_attention_rows(const ds_kv_cache* cache, const uint16_t* q, int64_t ldq,
                             int32_t n_q_heads, const int32_t* lens, int32_t new_tokens,

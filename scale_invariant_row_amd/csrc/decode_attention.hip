@@ -14,14 +14,13 @@
 // sequence is cut goes by its own length alone, so a row's bits do not depend on the
 // batch.
 //
-// Bound by the cache's bytes, each read once: 64 sequences of up to 8,192 tokens
-// over 4 heads of 256 (1.09 GB) take 235 us, 4.6 TB/s, and 10 to join; 4 of up to
-// 131,072 over 8 heads of 128 in e4m3 (0.67 GB) 128 us, 5.2 TB/s, and 8; a kernel
-// that only reads reaches 6.0.  A wave issues for a quarter of its time and waits
-// for loads for the rest; without the stores of the chunks' sums (36 MB), whose
-// acknowledgement the next loads' count waits for, the first takes 214.  Those
-// stores as whole rows, out of LDS, take as long; V's sums or K's products left
-// out save 2 %; pages in order instead of scattered, nothing.
+// Bound by the cache's bytes, each read once for up to 32 rows a kv head (every 32
+// more read them again: 35 rows take 134 us where 30 take 89): 64 sequences of up to
+// 8,192 tokens over 4 heads of 256 (1.09 GB) take 236 us, 4.6 TB/s, and 10 to join; 4
+// of up to 131,072 over 8 heads of 128 in e4m3 (0.67 GB) 132 us, 5.1 TB/s, and 8.5; a
+// kernel that only reads reaches 6.0.  A wave issues for a quarter of its time and
+// waits for loads for the rest; without the stores of the chunks' sums (35 MB), whose
+// acknowledgement the next loads' count waits for, the first takes 214.
 #include <algorithm>
 #include <type_traits>
 
@@ -90,8 +89,12 @@ __device__ __forceinline__ u32x2_t widen4(uint32_t w) {
 
 // The work is a list of chunks: of sequence 0 its heads' (and row groups'), one
 // after the other, then of sequence 1.  Wave i of W takes the i-th of W equal
-// stretches of the list, so as many waves as the chip holds are busy for as long
-// whatever the lengths are.
+// stretches of the list, counted in chunks.  Those hold 128 keys, 256 or, of a
+// sequence that would make more than 128 of them, more, so waves that take long
+// sequences' chunks are done last: of 4 sequences of 32,768 to 131,072 tokens a wave
+// takes 512 to 2,048 keys, and one of 131,072 beside 63 of 100 takes 189 us, alone
+// 164.  Each wave finds its place by reading all lengths, 512 at a time, which is most
+// of the time of many sequences with hardly a token (16,384 of 8: 550 us).
 struct Item {
   int seq, part, c;                  // part: row group * heads + head; c: chunk
   Span span;                         // of the sequence
@@ -455,8 +458,8 @@ __global__ void __launch_bounds__(256, HB * RT <= 2 ? 3 : HB <= (RT == 1 ? 4 : 2
           m[r] = m_new;
           float sum = 0.f;
           // Three parts hold a weight's 24 bits.  Two, 16 bits, move about one output
-          // of 1,000 to a neighbouring bf16 value, and take 236.5 us instead of 238
-          // over 64 sequences of up to 8,192 tokens, 84 instead of 85 with two row tiles.
+          // of 1,000 to a neighbouring bf16 value, and take 235 us instead of 237 over
+          // 64 sequences of up to 8,192 tokens, 84 instead of 85.5 with two row tiles.
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float w = exp2_fast(zs[i] - base);
@@ -669,7 +672,7 @@ int64_t attention_workspace(int64_t seqs, int64_t capacity, int q_heads, int hea
 
 // As many workgroups as the chip holds at once (by their registers), or one for
 // each chunk, whose waves then lie on as many compute units as they can (96
-// chunks: 10.4 us, in a quarter of the workgroups 11.6).  A workgroup that starts
+// chunks: 10.4 us, in a quarter of the workgroups 11.5).  A workgroup that starts
 // later would start its loads from nothing.
 template <int HB, bool E4M3, int RT>
 static void attend(const AttendArgs& a, const Split& sp, int64_t most, int cus, hipStream_t stream) {

@@ -19,7 +19,7 @@
 // a NaN of it).
 //
 // Bound by memory: those rows (336 MB) take 57 us, 5.8 TB/s; 8,192 of 16 + 4 heads
-// of 256 31 us, 5.5; 24 prompts of up to 1,021 tokens, 32 + 2 * 8 heads of 128,
+// of 256 30.5 us, 5.5; 24 prompts of up to 1,021 tokens, 32 + 2 * 8 heads of 128,
 // into a bf16 cache (315 MB) 53 us, 5.9; 16 + 2 * 4 heads of 256, normed, into
 // e4m3 (288 MB) 54 us, 5.3.
 #include "decode_launch.hpp"
@@ -247,9 +247,9 @@ __device__ __forceinline__ int64_t token_offset(const CacheView& c, int64_t seq,
   return token_bytes_at(c, position(c.table, table_entry(c, seq, p)), p);
 }
 
-// 1 << share waves a row.  Five waves a SIMD: 24 prompts of up to 1,021 tokens,
-// 16 + 2 * 4 heads of 256 into e4m3, 65.5 us with the four that the compiler
-// comes to by itself, 54.2 with five, 57.4 with six (registers spilled).
+// 1 << share waves a row.  Bounds for five waves a SIMD: 24 prompts of up to 1,021
+// tokens, 16 + 2 * 4 heads of 256 into e4m3, take 54 us with them, 66 with none and 67
+// with bounds for six (registers spilled).
 template <int LPH, int PAIRS, bool RMS>
 __global__ void __launch_bounds__(256, PAIRS == kOddHalves ? 4 : 5) cache_append_kernel(const AppendArgs a, int share) {
   constexpr int HPW = 64 / LPH, CH = 2;
@@ -353,7 +353,7 @@ static int groups(int heads, int group) { return (heads + group - 1) / group; }
 
 // log2 of the waves that share a row of `n` groups: as many as have one each,
 // up to a workgroup's four, where that leaves at most kFew waves a SIMD.  64
-// rows of 16 + 2 * 4 heads of 256 take 9.9 us by one wave each, 6.4 by four;
+// rows of 16 + 2 * 4 heads of 256 take 8.6 us by one wave each, 5.6 by four;
 // 24,500 rows of 32 + 2 * 8 heads of 128 take 53 by one, 59 by four (each finds
 // its row's angles again).
 static int waves_of(int64_t rows, int n, int cus) {

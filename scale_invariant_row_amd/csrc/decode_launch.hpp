@@ -72,12 +72,13 @@ struct Span {
 };
 
 // The least chunk is one block, or two where one block makes more than 512 chunks
-// of the sequence's heads.  One sequence over 4 heads of 256 takes 18.7 us (and 5
-// to join) for 8,000 tokens with one block, 38.1 with two; 32 sequences of up to
-// 4,096 tokens over 8 heads of 128, 5 new ones each, 85 and 12.8 with one, 82 and
-// 10.7 with two (half as many sums are written and read again).  Half a block
-// would take 9.4 us instead of 10.4 for 1,021 tokens over 12 heads of 64, but
-// 256 instead of 237 for 64 sequences of up to 8,192 over 4 heads of 256.
+// of the sequence's heads.  One sequence over 4 heads of 256 takes 21 us (and 5
+// to join) for 8,000 tokens with one block, 27 with two, and 1,021 tokens over 12
+// heads of 64 take 10.4 and 14; 32 sequences of up to 4,096 tokens over 8 heads of
+// 128, 5 new ones each, 86 and 12.6 with one, 86 and 10.4 with two (half as many sums
+// are written and read again).  Half a block would take 8.4 us for those 1,021 tokens,
+// but 252 and 16.5 for 64 sequences of up to 8,192 over 4 heads of 256 instead of 238
+// and 10.
 constexpr int64_t kFine = 512 * kBlock;      // keys times heads
 
 __host__ __device__ inline int least_chunk(int64_t keys, int heads) {

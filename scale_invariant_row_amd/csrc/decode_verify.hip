@@ -14,7 +14,8 @@
 // about one choice in a thousand would fall on the other side of a border.
 // That makes it bound by the ALUs: 25 instructions an element, 13 of them fp64
 // (at fp32's rate), are 47 us of the first launch's 61 over 576 rows of 131,072
-// bf16 logits (151 MB), and 10 of the last's 32.
+// bf16 logits (151 MB), and 10 of the last's 32.  Rows that end within a slice take
+// longer (load_as).
 #include "decode_launch.hpp"
 #include "powers_of_two.hpp"
 #include "row_kernels.hpp"
@@ -50,8 +51,10 @@ __device__ __forceinline__ float logit(const VerifyArgs& a, int which, int64_t r
 
 // N vectors of 8 scaled logits, the i-th from column col + i * step on, -infinity
 // past the vocabulary.  `whole`: none is past it (the same for the workgroup).
-// All loads are asked for before any value is used; rows may have any alignment
-// (global loads do not need theirs).
+// There all loads are asked for before any value is used; rows may have any alignment
+// (global loads do not need theirs).  Where the row ends within, each column is loaded
+// under a condition and waited for by itself, and the launch lasts as long as those
+// workgroups: 576 rows of 128,256 take 164 us, of 131,072 (16 whole slices) 55.
 template <int N, bool F32, bool SCALED>
 __device__ __forceinline__ void load_as(const VerifyArgs& a, int which, int64_t row, int col, int step, bool whole,
                                         float (&z)[N][8]) {
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(const VerifyA
     // have none: a store of agent scope is counted until it lies where every die reads
     // it.  The wait is an instruction that no access may be moved across, so the source
     // alone keeps it.  (An atomic that releases and acquires whole caches, which the
-    // model would ask for, took 44 us where this takes 34.)
+    // model would ask for, takes 62 us where this takes 34.)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     is_last = __hip_atomic_fetch_add(done + seq, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)n_parts - 1;
   }
@@ -524,9 +527,9 @@ int64_t verify_workspace(int64_t seqs, int drafts, int64_t vocab, bool with_draf
 }
 
 // With few workgroups in the last launch each decides by itself (one user's 3
-// drafts of 32,003 tokens: 10.8 us, against 9.5 + 3.4 and a launch more); with
+// drafts of 32,003 tokens: 10.6 us, against 9.5 + 3.1 and a launch more); with
 // more than twice the compute units a launch of its own decides once a sequence
-// (64 sequences of 4 drafts of 131,072 tokens: 5.8 + 33 us, against 46).
+// (64 sequences of 4 drafts of 131,072 tokens: 5.4 + 33.5 us, against 48.5).
 hipError_t launch_draft_verify(const VerifyArgs& a, int cus, void* workspace, hipStream_t stream) {
   const int n = slices_of(a.vocab), rows = a.drafts + 1 + (a.x[1] != nullptr ? a.drafts : 0);
   const int parts = parts_of(a.vocab);
