@@ -1330,6 +1330,10 @@ def ds_cache_attention_rows(cache: KvCache, q, lens, scale: Optional[float] = No
     up to its own, the last ``window`` of them if that is not 0; ``scale``:
     1 / sqrt(head_dim) if not given.  Returns out (bf16, like q), or (out, lse)
     with fp32 lse [rows, nq]; a row that sees nothing gets 0 and -infinity.
+
+    The call's scratch memory goes by what the page table allows (or the
+    window), not by the lengths; a KvCache with the table's first columns,
+    as many as the longest sequence needs, takes less and gives the same bits.
     """
     torch = _torch()
     desc = cache._here()

@@ -24,7 +24,7 @@ namespace dsr {
 
 constexpr int kSlice = 8192;          // columns a workgroup of the first launch takes
 constexpr int kPart = 4096;           // and of the last
-constexpr int kSumThreads = 256, kPickThreads = 512;
+constexpr int kSumThreads = 256, kPickThreads = 512;   // 256 at least: they fill ExpTable
 constexpr int kMaxRowsPerSeq = 72;    // >= 2 DS_MAX_DRAFTS + 1
 constexpr int kMaxSlices = 128;       // DS_MAX_VOCAB / kSlice
 constexpr int kMaxParts = 256;        // DS_MAX_VOCAB / kPart
@@ -123,6 +123,7 @@ __device__ __forceinline__ void load_logits(const VerifyArgs& a, int which, int6
 // table of 128 and a cubic, 12, are 2.2e-12 off and take as long.
 struct ExpTable {
   double t[256];
+  static_assert(kSumThreads >= 256 && kPickThreads >= 256);
   __device__ __forceinline__ void fill() {               // by 256 threads at least; a barrier follows
     if (threadIdx.x < 256) t[threadIdx.x] = kPowersOfTwo[threadIdx.x];
   }
