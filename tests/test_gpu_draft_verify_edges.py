@@ -101,3 +101,25 @@ def test_target_rows_that_say_nothing_refuse_whatever_the_random_number(B, certa
     c.check(got)
     assert host(got.accepted)[:5].tolist() == [0, 0, 1, 1, 2]
     assert host(got.tokens)[:2, 0].tolist() == [-1, -1] and np.isfinite(host(got.logp)).all()
+
+
+def test_acceptance_of_improbable_tokens_near_its_border(B):
+    """Down to e^-85, where e^z may be off by 2 + 85 / 3 units of 2^-53 and what
+    follows by 6: 37, under 5e-15."""
+    import torch
+    rng = np.random.default_rng(5)
+    z = -rng.uniform(8.0, 85.0, 1 << 22).astype(np.float32)
+    e = np.exp(z.astype(np.longdouble))
+    p = e / (1 + e)
+    u = p.astype(np.float32)
+    off = np.abs(u - p) / p
+    at = np.flatnonzero((off > 5e-15) & (off < 2e-12))
+    z, u, yes, n = z[at], u[at], u[at] < p[at], len(at)
+    assert n > 100
+    target = np.zeros((n, 2, 2), np.float32)
+    target[:, 0, 1] = z
+    announce("verify improbable tokens near the border of acceptance", n)
+    got = B.ds_draft_verify_rows(dev(target.reshape(2 * n, 2)), dev(np.ones((n, 1), np.int32)), dev(u[:, None]),
+                                 dev(np.full(n, 0.25, np.float32)))
+    torch.cuda.synchronize()
+    assert np.array_equal(host(got.accepted) == 1, yes)
